@@ -504,6 +504,125 @@ RGLRU_API rglru_status rglru_mqa_residual_block_prefill(
 RGLRU_API rglru_status rglru_carry_scan(int N, int B, int D, const float *H0, const float *H1, const float *h0,
                                         float *h_in, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving operators: one step of a decoder layer over a paged 8-bit cache.
+ *
+ * Next to the blocks above (prefill of whole sequences, bf16 rings, bf16
+ * weights) these carry a batch of sequences of different lengths, one token
+ * or a chunk of tokens each, with the bytes cut down: the residual's addition
+ * fused with the norm, 4-bit weights, and keys and values in 8 bits.
+ * rglru_paged_append and rglru_paged_attention let a prompt be processed in
+ * chunks that attend what earlier calls cached, which rglru_mqa_attention
+ * (its own tokens only) does not.
+ *
+ * 8-bit values are e4m3 codes with fp32 scales that are powers of two: a
+ * group of values x is held as code * 2^e, e the smallest exponent in [-100,
+ * 120] with max|x| <= 448 * 2^e; to nearest, ties to even; an infinity becomes
+ * +-448, a NaN stays one (it does not count for the maximum).
+ * Pointers are device pointers, 16-byte aligned, row-major; outputs must not
+ * overlap inputs except where a call says so.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * h = bf16(x + residual), residual_out = h, out = RMSNorm(h) as rglru_rmsnorm:
+ * the result of an addition followed by rglru_rmsnorm, in one pass.
+ *   x, residual, residual_out, out [M, N] bf16; weight [N] fp32; eps > 0;
+ *   N a multiple of 8 up to 16384.
+ * residual and residual_out may both be NULL: h = x.  residual_out may be x or
+ * residual itself.
+ */
+RGLRU_API rglru_status rglru_add_rmsnorm(int M, int N, const void *x, const void *residual, const float *weight,
+                                         float eps, void *residual_out, void *out, cudaStream_t stream);
+
+/*
+ * The same with an 8-bit output: out [M, N] e4m3 codes, out_scale [M, N /
+ * group] fp32, one scale for each group of channels (group 32, 64, 128 or 256,
+ * N a multiple of it).  The norm's result is rounded once, from fp32.
+ */
+RGLRU_API rglru_status rglru_add_rmsnorm_e4m3(int M, int N, int group, const void *x, const void *residual,
+                                              const float *weight, float eps, void *residual_out, void *out,
+                                              float *out_scale, cudaStream_t stream);
+
+/*
+ * A projection of few rows with 4-bit weights:
+ *   out[m, n] = sum_g s[n, g] sum_{k in g} (q[n, k] - 8) x[m, k] + bias[n]
+ *   W [N, K / 2] bytes: q in 0..15, the even k in the low half of a byte;
+ *   W_scale [N, K / group] bf16, group 32, 64 or 128, K a multiple of it;
+ *   A [M, K] bf16 with A_scale NULL, or e4m3 codes with A_scale [M, K /
+ *   a_group] fp32 powers of two, a_group 32, 64, 128 or 256 (the output of
+ *   rglru_add_rmsnorm_e4m3; other scales are rounded to 8 bits with the code's
+ *   value); bias [N] fp32 or NULL; out [M, N] bf16.
+ * 1 <= M <= 64 (more rows: RGLRU_ERR_UNSUPPORTED; rglru_linear is the call for
+ * those), any N up to 2^20, K up to 2^20.  The weights' integers and x enter
+ * the products exactly, sums are fp32, the output is rounded once.
+ */
+RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group, const void *A, const float *A_scale,
+                                       int a_group, const void *W, const void *W_scale, const float *bias, void *out,
+                                       cudaStream_t stream);
+
+/*
+ * The paged cache and the batch, for both calls below:
+ *   k_cache, v_cache [num_pages, Hkv, page_size, head_dim] e4m3 codes and
+ *     k_scale, v_scale [num_pages, Hkv] fp32: one scale for each page and head;
+ *     page_size 16, 32, 64 or 128, head_dim 128 or 256;
+ *   cu_tokens [S + 1] int32: the new tokens of sequence i are the rows
+ *     cu_tokens[i] .. cu_tokens[i + 1] - 1 (none, one or many);
+ *   ctx_len [S] int32: tokens of sequence i before them; new token t has
+ *     position ctx_len[i] + t;
+ *   block_table [S, max_pages] int32: position p is slot p % page_size of page
+ *     block_table[i, p / page_size]; entries that a call does not need
+ *     (pages before the window, pages past the end) are not read and may hold anything.
+ * max_new and max_total bound the lengths: cu_tokens[i + 1] - cu_tokens[i] <=
+ * max_new, ctx_len[i] plus that <= max_total <= max_pages * page_size.  The
+ * lengths and the table live on the device, so they are checked there: a
+ * sequence whose lengths break the bounds is skipped, a page number outside the
+ * pool is not touched (its tokens are not stored, or its keys not attended), and
+ * RGLRU_ERR_INVALID_ARG is recorded in the workspace (rglru_get_device_status).
+ * Rows behind cu_tokens[S] are left as they were.  1 <= rows <= 2^24,
+ * S <= 65535, H <= 256 a multiple of Hkv <= 64, max_total <= 2^30.
+ */
+
+/*
+ * Appends the new tokens' keys and values to the cache, with RoPE on the way:
+ *   qkv [rows, (H + 2 Hkv) * head_dim] bf16: query heads, key heads, value heads;
+ *   q_out [rows, H * head_dim] bf16: the rotated query heads.
+ * q and k are turned as in rglru_mqa_rope (pairs (x[i], x[i + head_dim / 2])
+ * by position * rope_base^(-2i / head_dim)); q is rounded to bf16, k and v to
+ * e4m3 from fp32.  The scale of a page entered at its first slot is that of the
+ * call's tokens in it.  A page entered past its first slot keeps the
+ * larger of the scale it had and that of the new tokens; when it grew, the
+ * slots before the first new one are rounded again at the new scale.  Slots
+ * behind the last new token are left as they were.  Every page that the call
+ * writes must be written for one sequence only.  The workspace (at least
+ * rglru_linear_workspace_size() bytes, zero-filled once) holds the status word.
+ */
+RGLRU_API rglru_status rglru_paged_append(
+    int rows, int S, int H, int Hkv, int head_dim, int page_size, int num_pages, int max_pages, int max_new,
+    int max_total, const void *qkv, const int32_t *cu_tokens, const int32_t *ctx_len, const int32_t *block_table,
+    float rope_base, void *q_out, void *k_cache, float *k_scale, void *v_cache, float *v_scale, void *workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of rglru_paged_attention, for any batch (0 on unsupported sizes). */
+RGLRU_API size_t rglru_paged_attention_workspace_size(int H, int Hkv, int head_dim);
+
+/*
+ * Attention of the new tokens over the cache, their own keys included (append
+ * them first):
+ *   out[t, h] = sum_p softmax_p(scale q[t, h] . k[p]) v[p],
+ *   pos_t - window < p <= pos_t, query head h reading head h / (H / Hkv).
+ * q, out [rows, H * head_dim] bf16 (q as rglru_paged_append gives it); window
+ * >= 1 (2^30 or more reaches every position); scale > 0.  Scores, sums and the
+ * output's accumulation are fp32; the probabilities enter the second product
+ * as f16.  A row with no key (bad pages only) gives zeros.  The workspace is
+ * zero-filled once and not shared by calls that can overlap.
+ */
+RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, int head_dim, int page_size,
+                                             int num_pages, int max_pages, int max_new, int max_total, int window,
+                                             float scale, const void *q, const int32_t *cu_tokens,
+                                             const int32_t *ctx_len, const int32_t *block_table, const void *k_cache,
+                                             const float *k_scale, const void *v_cache, const float *v_scale, void *out,
+                                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,7 +30,9 @@ SYMBOLS = ("rglru_version", "rglru_status_string", "rglru_workspace_size", "rglr
            "rglru_rmsnorm", "rglru_residual_block_workspace_size", "rglru_residual_block_prefill",
            "rglru_mqa_vt_size", "rglru_mqa_rope", "rglru_mqa_attention", "rglru_mqa_block_workspace_size",
            "rglru_mqa_block_prefill", "rglru_mqa_decode_workspace_size", "rglru_mqa_decode_step",
-           "rglru_mqa_residual_block_workspace_size", "rglru_mqa_residual_block_prefill", "rglru_carry_scan")
+           "rglru_mqa_residual_block_workspace_size", "rglru_mqa_residual_block_prefill", "rglru_carry_scan",
+           "rglru_add_rmsnorm", "rglru_add_rmsnorm_e4m3", "rglru_linear_w4", "rglru_paged_append",
+           "rglru_paged_attention_workspace_size", "rglru_paged_attention")
 
 _lib = None
 
@@ -117,6 +119,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rglru_mqa_residual_block_prefill.argtypes = [i, i, i, i, i] + [vp] * 13 + [ctypes.c_float, vp, vp, sz, vp]
     lib.rglru_carry_scan.restype = i
     lib.rglru_carry_scan.argtypes = [i, i, i] + [vp] * 4 + [vp]
+    f = ctypes.c_float
+    lib.rglru_add_rmsnorm.restype = i
+    lib.rglru_add_rmsnorm.argtypes = [i, i, vp, vp, vp, f, vp, vp, vp]
+    lib.rglru_add_rmsnorm_e4m3.restype = i
+    lib.rglru_add_rmsnorm_e4m3.argtypes = [i, i, i, vp, vp, vp, f, vp, vp, vp, vp]
+    lib.rglru_linear_w4.restype = i
+    lib.rglru_linear_w4.argtypes = [i, i, i, i, vp, vp, i, vp, vp, vp, vp, vp]
+    lib.rglru_paged_append.restype = i
+    lib.rglru_paged_append.argtypes = [i] * 10 + [vp] * 4 + [f] + [vp] * 6 + [sz, vp]
+    lib.rglru_paged_attention_workspace_size.restype = sz
+    lib.rglru_paged_attention_workspace_size.argtypes = [i, i, i]
+    lib.rglru_paged_attention.restype = i
+    lib.rglru_paged_attention.argtypes = [i] * 11 + [f] + [vp] * 10 + [sz, vp]
     _lib = lib
     return lib
 
@@ -838,3 +853,217 @@ def carry_scan(H0, H1, h0, h_in=None) -> torch.Tensor:
     if st != OK:
         raise RGLRUError(st, "rglru_carry_scan")
     return h_in
+
+
+# ---------------------------------------------------------------- serving operators over a paged 8-bit cache
+E4M3 = torch.float8_e4m3fn
+FULL_WINDOW = 1 << 30  # a window that reaches every position
+
+
+def _enqueue(name: str, dev: torch.device, *args) -> None:
+    """Runs the library call ``name`` on ``dev`` (made current for the launch) and its current stream."""
+    stream = _stream(dev)
+    fn = getattr(_lib or load(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != OK:
+        raise RGLRUError(st, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_args(x, residual, weight, residual_out):
+    N = x.shape[-1] if x.dim() else 0
+    if N == 0 or x.numel() == 0:
+        raise ValueError("x must be [..., N] with at least one row")
+    dev = x.device
+    _check(x, "x", x.shape, torch.bfloat16, dev)
+    _check(weight, "weight", (N,), torch.float32, dev)
+    if residual is not None:
+        _check(residual, "residual", x.shape, torch.bfloat16, dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        _check(residual_out, "residual_out", x.shape, torch.bfloat16, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    return x.numel() // N, N, dev, residual_out
+
+
+def add_rmsnorm(x, residual, weight, eps: float = 1e-6, out=None, residual_out=None):
+    """h = x + residual (bf16), out = RMSNorm(h) (rglru_add_rmsnorm); x, residual [..., N] bf16, weight
+    [N] fp32.  Returns (out, h); residual_out (h) may be x or residual.  Without a residual h is x."""
+    M, N, dev, residual_out = _norm_args(x, residual, weight, residual_out)
+    if out is None:
+        out = torch.empty_like(x)
+    _check(out, "out", x.shape, torch.bfloat16, dev)
+    _enqueue("rglru_add_rmsnorm", dev, M, N, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
+             _addr(residual_out), out.data_ptr())
+    return out, (x if residual is None else residual_out)
+
+
+def add_rmsnorm_e4m3(x, residual, weight, eps: float = 1e-6, group: int = 128, out=None, scale=None,
+                     residual_out=None):
+    """add_rmsnorm with an 8-bit output (rglru_add_rmsnorm_e4m3).  Returns (codes [..., N] float8_e4m3fn,
+    scale [..., N / group] fp32, h): the values are codes * scale, one scale a group of channels."""
+    M, N, dev, residual_out = _norm_args(x, residual, weight, residual_out)
+    if group < 1 or N % group != 0:
+        raise ValueError(f"N = {N} is not a multiple of group = {group}")
+    if out is None:
+        out = torch.empty(x.shape, dtype=E4M3, device=dev)
+    _check(out, "out", x.shape, E4M3, dev)
+    shape = (*x.shape[:-1], N // group)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=dev)
+    _check(scale, "scale", shape, torch.float32, dev)
+    _enqueue("rglru_add_rmsnorm_e4m3", dev, M, N, group, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
+             _addr(residual_out), out.data_ptr(), scale.data_ptr())
+    return out, scale, (x if residual is None else residual_out)
+
+
+def linear_w4(A, W, W_scale, bias=None, A_scale=None, out=None) -> torch.Tensor:
+    """out[m, n] = sum_k W_scale[n, k // group] * (q[n, k] - 8) * A[m, k] + bias[n] (rglru_linear_w4), 1 to 64 rows.
+    W [N, K / 2] uint8 holds q, two to a byte, the even k in the low half; W_scale [N, K / group] bf16; A [M, K]
+    bf16, or float8_e4m3fn with A_scale [M, K / a_group] (what add_rmsnorm_e4m3 gives); bias [N] fp32."""
+    if A.dim() != 2 or W.dim() != 2 or W_scale.dim() != 2 or (A_scale is not None and A_scale.dim() != 2):
+        raise ValueError("linear_w4: A must be [M, K], W [N, K / 2], W_scale [N, K / group], A_scale [M, K / a_group]")
+    M, K = A.shape
+    N = W.shape[0]
+    dev = A.device
+    _check(A, "A", (M, K), torch.bfloat16 if A_scale is None else E4M3, dev)
+    _check(W, "W", (N, K // 2), torch.uint8, dev)
+    G = W_scale.shape[1]
+    if M == 0 or N == 0 or G == 0 or K == 0 or K % G != 0:
+        raise ValueError(f"W_scale: {G} groups do not divide K = {K}, or a size is zero")
+    _check(W_scale, "W_scale", (N, G), torch.bfloat16, dev)
+    a_group = 0
+    if A_scale is not None:
+        GA = A_scale.shape[1]
+        if GA == 0 or K % GA != 0:
+            raise ValueError(f"A_scale: {GA} groups do not divide K = {K}")
+        _check(A_scale, "A_scale", (M, GA), torch.float32, dev)
+        a_group = K // GA
+    if bias is not None:
+        _check(bias, "bias", (N,), torch.float32, dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _check(out, "out", (M, N), torch.bfloat16, dev)
+    _enqueue("rglru_linear_w4", dev, M, N, K, K // G, A.data_ptr(), _addr(A_scale), a_group, W.data_ptr(),
+             W_scale.data_ptr(), _addr(bias), out.data_ptr())
+    return out
+
+
+@dataclass
+class PagedCache:
+    """Keys and values [pages, Hkv, page_size, D] float8_e4m3fn and their scales [pages, Hkv] fp32."""
+    k: torch.Tensor
+    k_scale: torch.Tensor
+    v: torch.Tensor
+    v_scale: torch.Tensor
+
+
+@dataclass
+class PagedBatch:
+    """New tokens of S sequences: cu_tokens [S + 1], ctx_len [S] (tokens before them) and block_table
+    [S, max_pages], int32 on the device; max_new and max_total bound the lengths of every sequence."""
+    cu_tokens: torch.Tensor
+    ctx_len: torch.Tensor
+    block_table: torch.Tensor
+    max_new: int
+    max_total: int
+
+
+def paged_cache(num_pages: int, heads: int = 1, page_size: int = 64, head_dim: int = 256, device="cuda") -> PagedCache:
+    """An empty cache of ``num_pages`` pages (zero codes, unit scales)."""
+    def codes():
+        return torch.zeros((num_pages, heads, page_size, head_dim), dtype=E4M3, device=device)
+
+    def scales():
+        return torch.ones((num_pages, heads), dtype=torch.float32, device=device)
+    return PagedCache(codes(), scales(), codes(), scales())
+
+
+def _paged_args(batch: PagedBatch, cache: PagedCache, dev):
+    if cache.k.dim() != 4:
+        raise ValueError("cache.k must be [pages, Hkv, page_size, D]")
+    P, Hkv, ps, D = shape = tuple(cache.k.shape)
+    _check(cache.k, "cache.k", shape, E4M3, dev)
+    _check(cache.v, "cache.v", shape, E4M3, dev)
+    _check(cache.k_scale, "cache.k_scale", (P, Hkv), torch.float32, dev)
+    _check(cache.v_scale, "cache.v_scale", (P, Hkv), torch.float32, dev)
+    if batch.ctx_len.dim() != 1 or batch.block_table.dim() != 2:
+        raise ValueError("ctx_len must be [S] and block_table [S, max_pages]")
+    S = batch.ctx_len.shape[0]
+    max_pages = batch.block_table.shape[1]
+    _check(batch.cu_tokens, "cu_tokens", (S + 1,), torch.int32, dev)
+    _check(batch.ctx_len, "ctx_len", (S,), torch.int32, dev)
+    _check(batch.block_table, "block_table", (S, max_pages), torch.int32, dev)
+    return S, Hkv, D, ps, P, max_pages
+
+
+def _paged_workspace(workspace, need, dev):
+    if workspace is None:
+        workspace = new_workspace(need, dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous, on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def paged_append(qkv, batch: PagedBatch, cache: PagedCache, rope_base: float = 10000.0, q_out=None,
+                 workspace=None) -> torch.Tensor:
+    """RoPE on the query and key heads of qkv [rows, (H + 2 Hkv) * D] bf16, the new keys and values into the
+    cache's pages in 8 bits (rglru_paged_append, in place); returns the rotated queries [rows, H * D] bf16.
+    A device-side refusal (bad lengths or page numbers) is read with device_status(workspace)."""
+    dev = qkv.device
+    S, Hkv, D, ps, P, max_pages = _paged_args(batch, cache, dev)
+    H = qkv.shape[1] // D - 2 * Hkv if qkv.dim() == 2 and D else 0
+    if H < 1:
+        raise ValueError("qkv must be [rows, (H + 2 Hkv) * D] with at least one query head")
+    rows = qkv.shape[0]
+    _check(qkv, "qkv", (rows, (H + 2 * Hkv) * D), torch.bfloat16, dev)
+    if q_out is None:
+        q_out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
+    _check(q_out, "q_out", (rows, H * D), torch.bfloat16, dev)
+    workspace, nb = _paged_workspace(workspace, 4096, dev)
+    _enqueue("rglru_paged_append", dev, rows, S, H, Hkv, D, ps, P, max_pages, batch.max_new, batch.max_total,
+             qkv.data_ptr(), batch.cu_tokens.data_ptr(), batch.ctx_len.data_ptr(), batch.block_table.data_ptr(),
+             rope_base, q_out.data_ptr(), cache.k.data_ptr(), cache.k_scale.data_ptr(), cache.v.data_ptr(),
+             cache.v_scale.data_ptr(), workspace.data_ptr(), nb)
+    return q_out
+
+
+def paged_attention_workspace_size(H: int, Hkv: int = 1, head_dim: int = 256) -> int:
+    n = int(load().rglru_paged_attention_workspace_size(H, Hkv, head_dim))
+    if n == 0:
+        raise RGLRUError(ERR_UNSUPPORTED, "paged_attention_workspace_size")
+    return n
+
+
+def paged_attention(q, batch: PagedBatch, cache: PagedCache, window: int = MQA_WINDOW, scale: float | None = None,
+                    out=None, workspace=None) -> torch.Tensor:
+    """Attention of the new tokens over the cache (rglru_paged_attention): q [rows, H * D] bf16 as paged_append
+    returns it; a token attends the ``window`` positions that end at its own; scale 1 / sqrt(D) unless given.
+    Returns out [rows, H * D] bf16 (rows behind the last sequence are not written)."""
+    dev = q.device
+    S, Hkv, D, ps, P, max_pages = _paged_args(batch, cache, dev)
+    H = q.shape[1] // D if q.dim() == 2 and D else 0
+    if H < 1:
+        raise ValueError("q must be [rows, H * D]")
+    rows = q.shape[0]
+    _check(q, "q", (rows, H * D), torch.bfloat16, dev)
+    if out is None:
+        out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
+    _check(out, "out", (rows, H * D), torch.bfloat16, dev)
+    if workspace is None:
+        workspace = new_workspace(paged_attention_workspace_size(H, Hkv, D), dev)
+    workspace, nb = _paged_workspace(workspace, 0, dev)
+    _enqueue("rglru_paged_attention", dev, rows, S, H, Hkv, D, ps, P, max_pages, batch.max_new, batch.max_total,
+             min(int(window), FULL_WINDOW), D ** -0.5 if scale is None else scale, q.data_ptr(),
+             batch.cu_tokens.data_ptr(), batch.ctx_len.data_ptr(), batch.block_table.data_ptr(), cache.k.data_ptr(),
+             cache.k_scale.data_ptr(), cache.v.data_ptr(), cache.v_scale.data_ptr(), out.data_ptr(),
+             workspace.data_ptr(), nb)
+    return out

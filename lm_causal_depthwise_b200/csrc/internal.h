@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <initializer_list>
 #include <mutex>
 
 #include "rglru.h"
@@ -85,6 +86,27 @@ size_t decode_workspace_bytes(int B, int D);
 rglru_status decode_step(const PrefillArgs &a);
 
 inline rglru_status cuda_status(cudaError_t e) { return e == cudaSuccess ? RGLRU_OK : RGLRU_ERR_CUDA; }
+
+// Argument checks of the serving operators: alignment, and overlap of the byte ranges of a call
+// (an empty range meets nothing).
+namespace args {
+inline bool al16(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+struct Span {
+    uintptr_t lo, hi;
+};
+inline Span span(const void *p, size_t bytes)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + bytes};
+}
+inline bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+inline bool clear(Span out, std::initializer_list<Span> others)
+{
+    for (const Span &s : others)
+        if (meet(out, s)) return false;
+    return true;
+}
+}  // namespace args
 
 // Per-device record of a one-time kernel attribute: the dynamic shared-memory
 // limit set by cudaFuncSetAttribute holds for the device that was current, so
