@@ -45,6 +45,13 @@ __device__ __forceinline__ uint32_t to_f16x2(uint32_t codes)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
     return r;
 }
+// four codes (the low two, the high two)
+__device__ __forceinline__ void to_f16x2x2(uint32_t codes, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
 __device__ __forceinline__ void to_f32x2(uint32_t codes, float &lo, float &hi)
 {
     const uint32_t h = to_f16x2(codes);

@@ -26,20 +26,34 @@ struct AttendArgs {
 // A unit is 16 rows (row = token * G + head in the group, G = H / Hkv) of one sequence and key/value head;
 // its work is the 64-key tiles of the sequence's attended range.  All units' tiles form one line, cut into
 // gridDim.x equal pieces: long and short sequences balance, and one long sequence spreads over every SM.
-constexpr int kRowTile = 16, kKeyTile = 64, kThreads = 128, kMinTiles = 2;
+constexpr int kRowTile = 16, kKeyTile = 64, kMinTiles = 2;
+constexpr int kConsumers = 128, kThreads = kConsumers + 32;
 constexpr int kSms = 148, kMaxCtas = 3 * kSms;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr size_t align_up_d(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+struct Meta {                // of one tile in the ring, written by the producer
+    float ks[4], lv[4];      // per 16 keys: k's scale, log2 of v's
+    int ok;                  // bit q: the 16 keys of group q can be attended by some row
+    int key0;                // position of the tile's first key
+    int flags;               // 1: first tile of its unit, 2: last tile of its unit
+    int row0, ctx;           // the sequence: first row, tokens before the call
+    int head, row, rows, left;  // the unit; tiles of it after this one
+};
 
 template <int D>
 struct Cfg {
-    static constexpr int kStages = D == 256 ? 3 : 4;
     static constexpr int kCtasPerSm = D == 256 ? 2 : 3;
-    static constexpr int kStageBytes = 2 * kKeyTile * D;
-    static constexpr int kSmem = kStages * kStageBytes;
+    static constexpr int kHalf = kKeyTile * 128;      // 64 keys x 128 channels (one swizzled box column)
+    static constexpr int kSlotBytes = kKeyTile * D;   // k or v of a tile
+    static constexpr int kSlots = D == 256 ? 5 : 7;
+    static constexpr int kQBytes = kRowTile * D * 2;  // a unit's rows as they come, and as f16 operands
+    static constexpr int kSmem = kSlots * kSlotBytes + 2 * kQBytes + 1024;
 };
+constexpr int kMeta = 8;  // k of tile t + kSlots - 1 takes the slot of v of tile t or a later one
 
-struct Plan {  // the unit that begins in a CTA's piece and does not end there
-    int parts, seq, unit, rows;
+struct Plan {  // the unit that begins in a CTA's piece and does not end there: its parts, rows and first row's place
+    int parts, rows, row0, row_head;  // row_head: first row (token * G + head in group) * 64 + key/value head
 };
 // Workspace: header, plans, then per CTA two partial results (slot 2 c: a unit begun in an earlier CTA; 2 c + 1: one begun
 // here) of 16 rows: m, mv, l, pad (float4) and O [16][D].
@@ -66,54 +80,31 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs &p, int i)
     return g;
 }
 
-// A place on the line of tiles.
-struct Cursor {
-    int seq, unit, tile;
-    Geometry g;
-};
-__device__ __forceinline__ void advance(const AttendArgs &p, Cursor &c)
-{
-    if (++c.tile < c.g.tiles) return;
-    c.tile = 0;
-    if (++c.unit < c.g.units) return;
-    c.unit = 0;
-    while (++c.seq < p.b.S) {
-        c.g = geometry(p, c.seq);
-        if (c.g.units > 0) return;
-    }
-}
-
-struct Unit {
-    int head, row, rows;    // key/value head, first row (token * G + head in group), rows
-    int pos0, pos1;         // positions of the first and last row
-    int lo, hi;             // keys any row attends
-};
-__device__ __forceinline__ Unit unit_of(const AttendArgs &p, const Cursor &c)
-{
-    const int G = p.b.H / p.b.Hkv, per_head = c.g.units / p.b.Hkv;
-    Unit u;
-    u.head = c.unit / per_head;
-    u.row = c.unit % per_head * kRowTile;
-    u.rows = min(kRowTile, c.g.n * G - u.row);
-    u.pos0 = c.g.ctx + u.row / G;
-    u.pos1 = c.g.ctx + (u.row + u.rows - 1) / G;
-    u.lo = max(0, u.pos0 - p.window + 1);
-    u.hi = u.pos1 + 1;
-    return u;
-}
-
 // ------------------------------------------------------------------------------------------------ pieces
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in)
+// A wait gives up after 2 s, records it and returns false; the caller goes on without waiting again (every loop is bounded),
+// and writes no result.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, WsHeader *ws, int where)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    const uint64_t t0 = sm100::globaltimer();
+    while (sm100::globaltimer() - t0 < kTimeoutNs)
+        if (sm100::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    atomicCAS(&ws->status, 0, (int)RGLRU_ERR_TIMEOUT);
+    atomicCAS(&ws->detail, 0, (int)(blockIdx.x << 8) | (where + 1));
+    return false;
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, WsHeader *ws, int where)
+{
+    return sm100::mbar_try_wait(bar, parity) || wait_slow(bar, parity, ws, where);
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(sm100::smem_u32(bar)), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -145,34 +136,61 @@ __device__ __forceinline__ long long piece_begin(long long total, int c, int n) 
 __device__ __forceinline__ int piece_of(long long total, long long t, int n) { return (int)(((t + 1) * n - 1) / total); }
 
 // ------------------------------------------------------------------------------------------------ the kernel
-// Four warps.  A 64-key tile of k and v (codes) arrives by cp.async in a ring.  S = Q K^T: warp w has the 16 keys of group w
+// One producer warp and four consumer warps.  The producer walks the piece's tiles, looks pages and scales up for eight tiles at
+// a time, and fetches the codes by TMA (128-byte swizzle) into a ring of slots, in the order of their use: k of tile 0, then k of
+// tile t + 1 and v of tile t.  S = Q K^T: consumer warp w has the 16 keys of group w
 // (one page, so one scale) and all 16 rows; the row maxima meet in shared memory, P goes
 // there as f16 in the layout of an mma operand, and O += P V: warp w has channels w D/4 .. of all keys, so that O is never summed
-// across warps.  Codes turn into f16 operands exactly, in registers.  k's scale multiplies the scores; v's enters the
+// across warps.  S of tile t + 1 is computed next to the softmax of tile t: one tile's chain (two barriers,
+// 16 dependent mma, exponentials) is latency, and the next one's products fill it.
+// Codes turn into f16 operands exactly, in registers (the e4m3 form of this mma is no faster: it runs
+// as conversions and f16 products, 5.0 cycles against 2.0).  k's scale multiplies the scores; v's enters the
 // exponent: P holds 2^(s - m + log2 vs - mv) with mv the running maximum of s - m + log2 vs, beside the softmax's own
 // maximum m and sum l = sum 2^(s - m), so that P keeps f16's bits whatever the pages' scales (mv is relative to m: a
 // large score would swallow log2 vs).
+//
+// Columns of an 8-key mma tile: column n is key n for even n, n ^ 4 for odd n.  With the swizzle (16-byte chunk c of
+// row r sits at c ^ (r & 7)) both the 16-byte reads of k (two rows a phase) and the 8-byte reads of v (four
+// rows a phase) then touch every bank once.
 template <int D>
-__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_attention_kernel(const AttendArgs p)
+__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm)
+rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap tm_k,
+                             const __grid_constant__ CUtensorMap tm_v)
 {
     using C = Cfg<D>;
-    constexpr int kStages = C::kStages, kChunks = D / 16, kKb = D / 64, kNt = D / 32, kSlice = D / 4;
-    constexpr int kRowsPerPass = kThreads / kChunks, kPasses = kKeyTile / kRowsPerPass;
-    extern __shared__ __align__(128) uint8_t ring[];
+    constexpr int kSlots = C::kSlots, kKb = D / 64, kNt = D / 32, kSlice = D / 4;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *qbuf = ring + kSlots * C::kSlotBytes;                   // the next unit's rows, bf16
+    uint4 *qfrag = reinterpret_cast<uint4 *>(qbuf + C::kQBytes);     // this unit's as mma operands: [D / 16][32 lanes]
+    __shared__ Meta meta[kMeta];
+    __shared__ uint64_t full[kSlots], empty[kSlots], q_full, q_empty;
     __shared__ float4 wmax[kRowTile], wlv;
+    __shared__ float qscale[kRowTile];
     __shared__ uint4 pbuf[4][32];
     __shared__ float lsum[4][kRowTile];
-    __shared__ long long scan[5];
-    __shared__ int where[4];
+    __shared__ long long scan[kThreads / 32];
+    __shared__ int where[3];
+    __shared__ Geometry where_g;
     const Batch &b = p.b;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, j = lane & 3;
-    const int G = b.H / b.Hkv, page_shift = 31 - __clz(b.page);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = b.H / b.Hkv;
+    sm100::griddep_launch_dependents();  // the joining kernel waits for this grid's end by itself
 
     // ---------------------------------------------------------------- this CTA's piece of the line
+    if (tid < kSlots) {
+        sm100::mbar_init(full + tid, 1);
+        sm100::mbar_init(empty + tid, kConsumers / 32);
+        if (tid == 0) sm100::mbar_init(&q_full, 1), sm100::mbar_init(&q_empty, kConsumers / 32);
+        sm100::mbar_fence_init();
+    }
     const int per = (b.S + kThreads - 1) / kThreads, s0 = min(b.S, tid * per), s1 = min(b.S, s0 + per);
     long long mine = 0;
+    Geometry g01[2] = {};  // of this thread's first two sequences: batches of up to 2 * kThreads are read once
     for (int i = s0; i < s1; ++i) {
         const Geometry g = geometry(p, i);
+        if (i == s0) g01[0] = g;
+        if (i == s0 + 1) g01[1] = g;
         mine += (long long)g.tiles * g.units;
     }
     long long inc = mine;
@@ -185,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
     __syncthreads();
     long long total = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += scan[w];
         total += scan[w];
     }
@@ -197,12 +215,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
         return;
     }
     const long long begin = piece_begin(total, cta, n_ctas), end = piece_begin(total, cta + 1, n_ctas);
+    const int count = (int)(end - begin);
     if (begin >= before && begin < before + mine) {
         long long at = before;
         for (int i = s0; i < s1; ++i) {
-            const Geometry g = geometry(p, i);
+            const Geometry g = i == s0 ? g01[0] : i == s0 + 1 ? g01[1] : geometry(p, i);
             const long long c = (long long)g.tiles * g.units;
             if (begin < at + c) {
+                where_g = g;
                 where[0] = i;
                 where[1] = (int)((begin - at) / g.tiles);
                 where[2] = (int)((begin - at) % g.tiles);
@@ -212,185 +232,264 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
         }
     }
     __syncthreads();
-    Cursor pc;  // the producer's place: the next tile to load
-    pc.seq = where[0], pc.unit = where[1], pc.tile = where[2];
-    pc.g = geometry(p, pc.seq);
-    Cursor cc = pc;  // the consumer's
-    const int count = (int)(end - begin);
-    float *parts = reinterpret_cast<float *>(reinterpret_cast<char *>(b.ws) + kWsHeaderBytes + align_up_d(kPlanBytes, 256));
-    Plan plan = {0, 0, 0, 0};
 
-    // ---------------------------------------------------------------- loads
-    const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
-    const int ld_row = tid / kChunks, ld_chunk = tid % kChunks;
-    int pages[4];                                  // of the next tile to load; -1: nothing to read there
-    Unit pu = unit_of(p, pc);
-    auto look_up = [&]() {
+    if (warp == kConsumers / 32) {
+        // ---------------------------------------------------------------- producer
+        const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile);
+        int seq = where[0], unit = where[1], tile = where[2], it = 0, units = 0, slot = 0, uses = 0;
+        Geometry g = where_g;
+        bool alive = true;
+        // a slot to fill: `boxes` of this lane's c1 (lanes 0 .. 3 with `leads`), k or v
+        auto fill = [&](const CUtensorMap *tm, bool leads, int c1) {
+            if (uses > 0 && alive) alive = wait(empty + slot, (uint32_t)(uses - 1) & 1u, b.ws, 0);
+            const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, leads));
+            if (lane == 0) mbar_expect(full + slot, n * (uint32_t)box * D);
+            __syncwarp();
+            if (leads) {
+                uint8_t *dst = ring + slot * C::kSlotBytes + 16 * lane * 128;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int p0 = (pc.g.tile0 + pc.tile) * kKeyTile + 16 * q;
-            pages[q] = p0 + 16 > pu.lo && p0 < pu.hi ? b.table[(size_t)pc.seq * b.max_pages + (p0 >> page_shift)] : -2;
-        }
-    };
-    float ksr[kStages], lvr[kStages];              // scales of this warp's 16 keys, one entry a tile in flight
-    auto issue = [&](int stage) {
-        const uint32_t dk = ring_addr + stage * C::kStageBytes, dv = dk + kKeyTile * D;
-        const int key0 = (pc.g.tile0 + pc.tile) * kKeyTile;
-        float ks = 0.f, vs = 0.f;
-        bool mine_ok = false;
-        size_t at[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (pages[q] != -2 && (pages[q] < 0 || pages[q] >= b.num_pages)) {
-                paged::record_invalid(b.ws);
-                pages[q] = -2;
+                for (int x = 0; x < D / 128; ++x) sm100::tma_load_2d(dst + x * C::kHalf, tm, full + slot, x * 128, c1);
             }
-            at[q] = (size_t)(pages[q] < 0 ? 0 : pages[q]) * b.Hkv + pu.head;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (q == warp && pages[q] >= 0) ks = p.ks[at[q]], vs = p.vs[at[q]], mine_ok = true;
-#pragma unroll
-        for (int r = 0; r < kPasses; ++r) {
-            const int row = r * kRowsPerPass + ld_row, q = r * kRowsPerPass / 16;   // 16 keys: one page
-            const int key = key0 + row;
-            const bool in = pages[q] >= 0 && key >= pu.lo && key < pu.hi;
-            const size_t off = in ? ((at[q] << page_shift) + (key & (b.page - 1))) * D + ld_chunk * 16 : 0;
-            cp16(dk + row * D + ((ld_chunk ^ ((row & 1) << 2)) << 4), p.k + off, in);
-            cp16(dv + row * D + ((ld_chunk ^ (((row >> 1) & 3) << 1)) << 4), p.v + off, in);
-        }
-        ksr[kStages - 1] = ks, lvr[kStages - 1] = mine_ok ? log2f(vs) : -INFINITY;
-        advance(p, pc);
-    };
-    int loaded = 0;
-    look_up();
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-#pragma unroll
-        for (int q = 0; q + 1 < kStages; ++q) ksr[q] = ksr[q + 1], lvr[q] = lvr[q + 1];
-        if (loaded < count) {
-            issue(s);
-            if (++loaded < count) {
-                pu = unit_of(p, pc);
-                look_up();
+        };
+        auto filled = [&]() {
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(full + slot);
+            if (++slot == kSlots) slot = 0, ++uses;
+        };
+        bool v_leads = false;  // of the tile whose v comes next
+        int v_c1 = 0;
+        for (; it < count; ++units) {
+            const int per_head = g.units / b.Hkv, head = unit / per_head, row = unit % per_head * kRowTile;
+            const int rows = min(kRowTile, g.n * G - row);
+            const int lo = max(0, g.ctx + row / G - p.window + 1), hi = g.ctx + (row + rows - 1) / G + 1;
+            const int tiles = min(g.tiles - tile, count - it);  // of this unit, in this piece
+            // its query rows, once the consumers have turned the last unit's into operands
+            if (units > 0 && alive) alive = wait(&q_empty, (uint32_t)(units - 1) & 1u, b.ws, 3);
+            if (lane == 0) sm100::mbar_arrive_expect_tx(&q_full, (uint32_t)rows * D * 2);
+            __syncwarp();
+            if (lane < rows) {
+                const int r = row + lane;
+                sm100::bulk_load(qbuf + lane * D * 2, p.q + ((size_t)(g.row0 + r / G) * b.H + head * G + r % G) * D, D * 2,
+                                 &q_full);
+            }
+            for (int t0 = 0; t0 < tiles; t0 += 8) {
+                // lane: group lane % 4 of tile t0 + lane / 4
+                const int q = lane & 3, key0 = (g.tile0 + tile + t0 + (lane >> 2)) * kKeyTile, key = key0 + 16 * q;
+                int page = -1;
+                float ks = 0.f, vs = 0.f;
+                const int bk = key & ~(box - 1);  // the box's first key
+                const bool wanted = t0 + (lane >> 2) < tiles && bk + box > lo && bk < hi;
+                if (wanted) {
+                    page = b.table[(size_t)seq * b.max_pages + (key >> page_shift)];
+                    if (page < 0 || page >= b.num_pages) {
+                        paged::record_invalid(b.ws);
+                        page = -1;
+                    }
+                }
+                const size_t at = (size_t)max(page, 0) * b.Hkv + head;
+                if (page >= 0) ks = p.ks[at], vs = p.vs[at];
+                const bool ok = page >= 0 && key + 16 > lo && key < hi;
+                const int leads = page >= 0 && key == bk;
+                const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+                const int c1 = (int)((at << page_shift) + (key & (b.page - 1)));
+                for (int t = 0; t < min(8, tiles - t0); ++t, ++it) {
+                    const bool k_leads = __shfl_sync(0xffffffffu, leads, 4 * t + q) != 0 && lane < 4;
+                    const int k_c1 = __shfl_sync(0xffffffffu, c1, 4 * t + q);
+                    fill(&tm_k, k_leads, k_c1);
+                    if ((lane >> 2) == t) {
+                        Meta &mt = meta[it % kMeta];
+                        mt.ks[q] = ks;
+                        mt.lv[q] = ok ? log2f(vs) : 0.f;
+                        if (q == 0) {
+                            mt.ok = (int)((oks >> (4 * t)) & 0xfu);
+                            mt.key0 = key0;
+                            const int left = g.tiles - 1 - (tile + t0 + t);
+                            mt.flags = (tile + t0 + t == 0 ? 1 : 0) | (left == 0 ? 2 : 0) | (t0 + t == 0 ? 4 : 0);
+                            mt.row0 = g.row0, mt.ctx = g.ctx, mt.head = head;
+                            mt.row = row, mt.rows = rows, mt.left = left;
+                        }
+                    }
+                    filled();
+                    if (it > 0) {
+                        fill(&tm_v, v_leads, v_c1);
+                        filled();
+                    }
+                    v_leads = k_leads, v_c1 = k_c1;
+                }
+            }
+            tile = 0;
+            ++unit;
+            if (unit == g.units && it < count) {
+                unit = 0;
+                do g = geometry(p, ++seq); while (g.units == 0);
             }
         }
-        cp_commit();
+        fill(&tm_v, v_leads, v_c1);
+        filled();
+        // no copy is in flight when the CTA ends
+        for (int k = 0; k < kSlots; ++k) {  // the slots' last uses, oldest first
+            if (uses > 0 || k < slot) {
+                const int x = uses > 0 ? (slot + k) % kSlots : k;
+                wait(full + x, (uint32_t)(x < slot ? uses : uses - 1) & 1u, b.ws, 1);
+            }
+        }
+        wait(&q_full, (uint32_t)(units - 1) & 1u, b.ws, 1);
+        return;
     }
 
-    // ---------------------------------------------------------------- tiles
-    uint32_t qf[kKb][4][4];
-    float acc[kNt][4], m[2], mv[2], l[2], qs[2];
+    // ---------------------------------------------------------------- consumers
+    const int quad = lane >> 2, j = lane & 3;
+    float *parts = reinterpret_cast<float *>(reinterpret_cast<char *>(b.ws) + kWsHeaderBytes + align_up_d(kPlanBytes, 256));
+    Plan plan = {0, 0, 0, 0};
+    const int kq = quad & 1 ? quad ^ 4 : quad;                 // this thread's key in an 8-key tile (row of k)
+    const int je = 2 * j, jo = (2 * j + 1) ^ 4;                // keys of the score columns 2j, 2j + 1 (rows of v)
+    const int k_off = (warp * 16 + kq) * 128 + ((j ^ kq) << 4);
+    // this warp's channels of v: first byte of the thread's kNt, in its 128-byte row
+    const int v_byte = (warp * kSlice + quad * kNt) & 127;
+    const int v_half = (warp * kSlice) / 128 * C::kHalf;
+    const int v_off[2] = {v_half + je * 128 + (((v_byte >> 4) ^ (je & 7)) << 4) + (v_byte & 15),
+                          v_half + jo * 128 + (((v_byte >> 4) ^ (jo & 7)) << 4) + (v_byte & 15)};
+    float acc[kNt][4], m[2], mv[2], l[2], qs[2], s[2][4];
     int pos[2];
-    Unit cu = {};
-    bool start = true;
-    int unit_first = 0;  // whether the piece holds the unit's first tile
-    for (int it = 0; it < count; ++it) {
-        cp_wait<kStages - 2>();
-        __syncthreads();
+    int pos_first = 0, pos_last = 0, unit_first = 0, slot = 0;
+    uint32_t phase = 0;
+    bool alive = true;
+    auto take = [&]() {  // the next slot of the ring, full
+        if (alive) alive = wait(full + slot, phase, b.ws, 2);
+        return ring + slot * C::kSlotBytes;
+    };
+    auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(empty + slot);
+        if (++slot == kSlots) slot = 0, phase ^= 1u;
+    };
+    // A unit's rows as f16 operands, each row times a power of two that brings its largest exponent to 2^13: every bf16
+    // down to 2^-27 of it is a normal f16.  Warp w converts the 64 channels of step w.
+    auto load_queries = [&](int rows, uint32_t turn) {
+        if (alive) alive = wait(&q_full, turn & 1u, b.ws, 4);
 #pragma unroll
-        for (int q = 0; q + 1 < kStages; ++q) ksr[q] = ksr[q + 1], lvr[q] = lvr[q + 1];
-        if (loaded < count) {
-            issue((it + kStages - 1) % kStages);
-            if (++loaded < count) {
-                pu = unit_of(p, pc);
-                look_up();
+        for (int h = 0; h < 2; ++h) {
+            const int r = quad + 8 * h;
+            const bool live = r < rows;
+            const uint4 *src = reinterpret_cast<const uint4 *>(qbuf + r * D * 2 + 32 * j);
+            uint32_t top = 0;
+#pragma unroll
+            for (int kb = 0; kb < 2 * kKb; ++kb) {
+                const uint4 v = live ? src[(kb >> 1) * 8 + (kb & 1)] : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7f800000u, w[x] & 0x7f800000u));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            int e = min(100, max(-100, (int)(top >> 23) - 127 - 13));
+            if (top == 0) e = 0;
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (warp == 0 && j == 0) qscale[r] = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+            if (warp < kKb) {
+                const uint4 v0 = live ? src[warp * 8] : make_uint4(0, 0, 0, 0), v1 = live ? src[warp * 8 + 1] : make_uint4(0, 0, 0, 0);
+                const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(qfrag + (warp * 4 + x) * 32 + lane);
+                    dst[h] = pack_f16(bf_lo(w[2 * x]) * f, bf_hi(w[2 * x]) * f);
+                    dst[2 + h] = pack_f16(bf_lo(w[2 * x + 1]) * f, bf_hi(w[2 * x + 1]) * f);
+                }
             }
         }
-        cp_commit();
-
-        if (start) {  // a new unit: its queries as operands, its sums empty
-            start = false;
-            unit_first = cc.tile == 0;
-            cu = unit_of(p, cc);
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&q_empty);
+        consumer_sync();
+    };
+    // raw scores of this warp's 16 keys of the next tile
+    auto scores = [&](float (&s)[2][4]) {
+        const uint8_t *st = take();
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb) {
+            uint32_t w[2][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const uint4 c = *reinterpret_cast<const uint4 *>(st + (kb >> 1) * C::kHalf + nt * 1024 +
+                                                                 (kb & 1 ? k_off ^ 64 : k_off));
+                w[nt][0] = c.x, w[nt][1] = c.y, w[nt][2] = c.z, w[nt][3] = c.w;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint4 qa = qfrag[(kb * 4 + x) * 32 + lane];
+                const uint32_t a[4] = {qa.x, qa.y, qa.z, qa.w};
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    uint32_t b0, b1;
+                    e4m3::to_f16x2x2(w[nt][x], b0, b1);
+                    mma_f16(s[nt], a, b0, b1);
+                }
+            }
+        }
+        release();
+    };
+    uint32_t units = 0;
+    if (alive) alive = wait(full, 0, b.ws, 2);  // tile 0's k, and with it its meta
+    load_queries(meta[0].rows, units++);
+    scores(s);
+    for (int it = 0; it < count; ++it) {
+        const Meta &mt = meta[it % kMeta];
+        if (mt.flags & 4) {  // the unit's first tile in this piece: its sums are empty
+            unit_first = mt.flags & 1;
+            pos_first = mt.ctx + mt.row / G;
+            pos_last = mt.ctx + (mt.row + mt.rows - 1) / G;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = quad + 8 * h;
-                const bool live = r < cu.rows;
-                const int row = cu.row + (live ? r : 0);
-                pos[h] = cc.g.ctx + row / G;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    p.q + ((size_t)(cc.g.row0 + row / G) * b.H + cu.head * G + row % G) * D + 16 * j);
-                uint4 v[kKb][2];
-                uint32_t top = 0;
-#pragma unroll
-                for (int kb = 0; kb < kKb; ++kb) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        v[kb][e] = live ? src[kb * 8 + e] : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {v[kb][e].x, v[kb][e].y, v[kb][e].z, v[kb][e].w};
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7f800000u, w[x] & 0x7f800000u));
-                    }
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the row's largest exponent to 2^13: every bf16 down to 2^-27 of it is a normal f16
-                int e = min(100, max(-100, (int)(top >> 23) - 127 - 13));
-                if (top == 0) e = 0;
-                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                qs[h] = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                for (int kb = 0; kb < kKb; ++kb) {
-                    const uint32_t w[8] = {v[kb][0].x, v[kb][0].y, v[kb][0].z, v[kb][0].w,
-                                           v[kb][1].x, v[kb][1].y, v[kb][1].z, v[kb][1].w};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        qf[kb][s][h] = pack_f16(bf_lo(w[2 * s]) * f, bf_hi(w[2 * s]) * f);
-                        qf[kb][s][2 + h] = pack_f16(bf_lo(w[2 * s + 1]) * f, bf_hi(w[2 * s + 1]) * f);
-                    }
-                }
+                pos[h] = mt.ctx + (mt.row + min(r, mt.rows - 1)) / G;
+                qs[h] = qscale[r];
                 m[h] = mv[h] = -INFINITY;
                 l[h] = 0.f;
             }
 #pragma unroll
             for (int t = 0; t < kNt; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
         }
-        const uint8_t *sk = ring + (it % kStages) * C::kStageBytes, *sv = sk + kKeyTile * D;
-        const int key0 = (cc.g.tile0 + cc.tile) * kKeyTile;
-
-        // S of this warp's 16 keys
-        float s[2][4] = {};
-#pragma unroll
-        for (int kb = 0; kb < kKb; ++kb) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const int row = warp * 16 + nt * 8 + quad;
-                const uint4 c = *reinterpret_cast<const uint4 *>(sk + row * D + (((kb * 4 + j) ^ ((row & 1) << 2)) << 4));
-                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mma_f16(s[nt], qf[kb][x], e4m3::to_f16x2(w[x] & 0xffffu), e4m3::to_f16x2(w[x] >> 16));
-            }
-        }
-        const float ks = ksr[0], lv = lvr[0];
-        const bool ok = lv != -INFINITY || ks != 0.f;
-        // whether some key of the tile is outside some row's range (rows of one token: outside keys were never loaded, but
-        // they must not be weighted either)
-        const bool edge = key0 < cu.pos1 - p.window + 1 || key0 + kKeyTile - 1 > cu.pos0 || !ok;
+        const int key0 = mt.key0, okm = mt.ok;
+        const float ks = mt.ks[warp], lv = mt.lv[warp];
+        // whether some key of the tile is outside some row's range, or was not loaded
+        const bool edge = okm != 15 || key0 < pos_last - p.window + 1 || key0 + kKeyTile - 1 > pos_first;
         float tmax[2] = {-INFINITY, -INFINITY};
+        const float qk[2] = {qs[0] * ks, qs[1] * ks};
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[nt][e] *= qs[e >> 1] * ks;
-                if (edge) {
-                    const int key = key0 + warp * 16 + nt * 8 + 2 * j + (e & 1);
+            for (int e = 0; e < 4; ++e) s[nt][e] *= qk[e >> 1];
+        if (edge) {
+            const bool ok = (okm >> warp) & 1;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = key0 + warp * 16 + nt * 8 + (e & 1 ? jo : je);
                     if (!ok || key > pos[e >> 1] || key <= pos[e >> 1] - p.window) s[nt][e] = -INFINITY;
                 }
-                tmax[e >> 1] = fmaxf(tmax[e >> 1], s[nt][e]);
-            }
         }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tmax[e >> 1] = fmaxf(tmax[e >> 1], s[nt][e]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], 1));
             tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], 2));
-            if (j == 0) {
-                reinterpret_cast<float *>(&wmax[quad + 8 * h])[warp] = tmax[h];
-            }
+            if (j == 0) reinterpret_cast<float *>(&wmax[quad + 8 * h])[warp] = tmax[h];
         }
-        if (lane == 0) reinterpret_cast<float *>(&wlv)[warp] = ok ? lv : 0.f;
-        __syncthreads();
+        if (lane == 0) reinterpret_cast<float *>(&wlv)[warp] = lv;
+        consumer_sync();
+        float sn[2][4] = {};
+        if (it + 1 < count) {
+            if (mt.left == 0) {  // another unit follows: every warp is done with the old operands
+                if (alive) alive = wait(full + slot, phase, b.ws, 2);
+                load_queries(meta[(it + 1) % kMeta].rows, units++);
+            }
+            scores(sn);
+        }
         float f[2];
         bool moved = false;
         uint32_t pk[4];
@@ -406,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
             f[h] = sm100::ex2_approx(mv[h] + step - vz);
             moved |= f[h] != 1.f;
             m[h] = m1, mv[h] = v1;
-            const float d = ok ? lv - vz : 0.f;
+            const float d = lv - vz;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
                 const float s0v = s[nt][2 * h] - mz, s1v = s[nt][2 * h + 1] - mz;
@@ -419,20 +518,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
 #pragma unroll
             for (int t = 0; t < kNt; ++t) acc[t][0] *= f[0], acc[t][1] *= f[0], acc[t][2] *= f[1], acc[t][3] *= f[1];
         }
-        __syncthreads();
+        consumer_sync();
+        const uint8_t *st = take();
 
-        // O += P V for this warp's channels: thread's 8 (D = 256; 4) channels of the keys 2j, 2j + 1, 2j + 8, 2j + 9
-        const bool mixed = edge && cu.pos0 != cu.pos1;  // rows that do not see the same keys
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const uint4 pa = pbuf[kk][lane];
-            const uint32_t a[4] = {pa.x, pa.y, pa.z, pa.w};
-            uint32_t v[4][kNt / 4];
+        // O += P V for this warp's channels: 16 keys a step, the thread's kNt channels of four of them
+        auto load_v = [&](int kk, uint32_t (&v)[4][kNt / 4]) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int row = kk * 16 + 2 * j + (q & 1) + (q >> 1) * 8;
-                const int byte = warp * kSlice + quad * kNt;
-                const uint8_t *src = sv + row * D + (((byte >> 4) ^ (((row >> 1) & 3) << 1)) << 4) + (byte & 15);
+                const uint8_t *src = st + v_off[q & 1] + kk * 2048 + (q >> 1) * 1024;
                 if (kNt == 8) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(src);
                     v[q][0] = w.x, v[q][kNt / 4 - 1] = w.y;
@@ -440,40 +533,58 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
                     v[q][0] = *reinterpret_cast<const uint32_t *>(src);
                 }
             }
-            uint32_t bad[4][kNt / 4];
-            bool any = false;
-            if (mixed) {  // a NaN may only reach the rows that see its key: it is taken out of the product
+        };
+        auto times_v = [&](int kk, const uint32_t (&v)[4][kNt / 4]) {
+            const uint4 pa = pbuf[kk][lane];
+            const uint32_t a[4] = {pa.x, pa.y, pa.z, pa.w};
+#pragma unroll
+            for (int x = 0; x < kNt / 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t c0[2], c1[2];
+                    e4m3::to_f16x2x2(__byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140), c0[0], c0[1]);
+                    e4m3::to_f16x2x2(__byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140), c1[0], c1[1]);
+                    mma_f16(acc[4 * x + 2 * y], a, c0[0], c1[0]);
+                    mma_f16(acc[4 * x + 2 * y + 1], a, c0[1], c1[1]);
+                }
+        };
+        if (!edge) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t v[4][kNt / 4];
+                load_v(kk, v);
+                times_v(kk, v);
+            }
+        } else {
+            // slots that no row attends may hold anything, and rows may see different keys: a NaN may only reach the
+            // rows that see its key, so it is taken out of the product
+#pragma unroll 1
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t v[4][kNt / 4], bad[4][kNt / 4], any = 0;
+                load_v(kk, v);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int x = 0; x < kNt / 4; ++x) {
                         bad[q][x] = nan_bytes(v[q][x]);
                         v[q][x] &= ~bad[q][x];
-                        any |= bad[q][x] != 0;
+                        any |= bad[q][x];
                     }
-                any = __any_sync(0xffffffffu, any);
-            }
-#pragma unroll
-            for (int x = 0; x < kNt / 4; ++x) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const uint32_t b0 = __byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140);
-                    const uint32_t b1 = __byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140);
-                    mma_f16(acc[4 * x + 2 * y], a, e4m3::to_f16x2(b0 & 0xffffu), e4m3::to_f16x2(b1 & 0xffffu));
-                    mma_f16(acc[4 * x + 2 * y + 1], a, e4m3::to_f16x2(b0 >> 16), e4m3::to_f16x2(b1 >> 16));
-                }
-            }
-            if (mixed && any) {
+                times_v(kk, v);
+                if (!__any_sync(0xffffffffu, any != 0)) continue;
                 // rows that see a NaN: the product of "sees" and "is NaN" is positive there
                 uint32_t see[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
-                        const int key = key0 + kk * 16 + nt * 8 + 2 * j;
-                        const bool s0v = key <= pos[h] && key > pos[h] - p.window;
-                        const bool s1v = key + 1 <= pos[h] && key + 1 > pos[h] - p.window;
-                        see[2 * nt + h] = (s0v ? 0x3c00u : 0u) | (s1v ? 0x3c000000u : 0u);
+                        uint32_t w = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + kk * 16 + nt * 8 + (e ? jo : je);
+                            if (((okm >> kk) & 1) && key <= pos[h] && key > pos[h] - p.window) w |= 0x3c00u << (16 * e);
+                        }
+                        see[2 * nt + h] = w;
                     }
 #pragma unroll
                 for (int x = 0; x < kNt / 4; ++x)
@@ -492,27 +603,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
         }
 
         // ---------------------------------------------------------------- the unit's end, or the piece's
-        const bool last = cc.tile + 1 == cc.g.tiles;
+        const bool last = (mt.flags & 2) != 0;
         if (last || it + 1 == count) {
+            const int urow = mt.row, urows = mt.rows, row0 = mt.row0, head = mt.head;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
                 if (j == 0) lsum[warp][quad + 8 * h] = l[h];
             }
-            __syncthreads();
+            consumer_sync();
             const bool whole = unit_first && last;
             float *slot = parts + ((size_t)cta * 2 + (unit_first ? 1 : 0)) * part_floats(D);
-            if (!whole && unit_first) {
-                // the piece ends inside the unit, which began here: the later CTAs with a part of it
-                const long long unit_end = end + (cc.g.tiles - 1 - cc.tile);
-                plan = {piece_of(total, unit_end - 1, n_ctas) - cta + 1, cc.seq, cc.unit, cu.rows};
-            }
+            if (!whole && unit_first)  // the unit began here and goes on: the later CTAs with a part of it
+                plan = {piece_of(total, end + mt.left - 1, n_ctas) - cta + 1, urows, row0, urow * 64 + head};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = quad + 8 * h;
                 const float lt = (lsum[0][r] + lsum[1][r]) + (lsum[2][r] + lsum[3][r]);
-                if (r >= cu.rows) continue;
+                if (r >= urows || !alive) continue;
                 const int c0 = warp * kSlice + 2 * kNt * j;  // 2 kNt contiguous channels
                 if (whole) {
                     const float o = lt == 0.f ? 0.f : sm100::ex2_approx(finite_or_0(mv[h])) / lt;
@@ -522,9 +631,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
                         const int e = 2 * t / kNt, x = 2 * t % kNt;  // channel 2 t of the thread's 2 kNt
                         w[t] = pack_bf16(acc[x][2 * h + e] * o, acc[x + 1][2 * h + e] * o);
                     }
-                    const int row = cu.row + r;
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        p.out + ((size_t)(cc.g.row0 + row / G) * b.H + cu.head * G + row % G) * D + c0);
+                    const int row = urow + r;
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)(row0 + row / G) * b.H + head * G + row % G) * D + c0);
 #pragma unroll
                     for (int t = 0; t < kNt / 4; ++t) dst[t] = make_uint4(w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]);
                 } else {
@@ -537,108 +645,201 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) rglru_paged_atte
                     }
                 }
             }
-            start = true;
         }
-        if (it + 1 < count) advance(p, cc);
+        release();  // v's slot, and with it the tile's meta
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = sn[nt][e];
     }
     if (tid == 0) plans[cta] = plan;
 }
 
-// Joins the parts of the units that were cut: an item is one row and 64 channels of such a unit; warps take
-// every eighth part, in an order that does not depend on which CTA was done first.
+// Joins the parts of the units that were cut, in their order along the line, whichever CTA was done first.  Units of few parts:
+// a warp takes a row.  Units of many parts (a long sequence over many SMs): a CTA takes 64 channels of a row, its
+// warps every eighth part.  Each CTA lists the items from the plans (one scan) and takes every gridDim.x-th.
+constexpr int kFewParts = 24, kJoinThreads = 1024;
+
 template <int D>
-__global__ void __launch_bounds__(256) rglru_paged_combine_kernel(const AttendArgs p, int n)
+__global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const AttendArgs p, int n)
 {
-    constexpr int kSlices = D / 64;
-    __shared__ int first[kMaxCtas + 1];
-    __shared__ int sums[8];
-    __shared__ float2 o[8][32];
-    __shared__ float red[8][3];
+    constexpr int kSlices = D / 64, kVec = D / 128, kWarps = kJoinThreads / 32;
+    constexpr int kBatch = (kMaxCtas + 2 * kWarps - 1) / (2 * kWarps);  // parts a half warp takes of a long unit
+    __shared__ int first[2][kMaxCtas + 1];  // running item counts: rows of short units, slices of long ones
+    __shared__ int sums[2][kWarps];
+    __shared__ Plan list[kMaxCtas];
+    __shared__ float4 o[kWarps][16];
+    __shared__ float red[kWarps][3];
     const Batch &b = p.b;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = b.H / b.Hkv;
     const Plan *plans = reinterpret_cast<const Plan *>(reinterpret_cast<const char *>(b.ws) + kWsHeaderBytes);
     const float *parts =
         reinterpret_cast<const float *>(reinterpret_cast<const char *>(b.ws) + kWsHeaderBytes + align_up_d(kPlanBytes, 256));
-    int have[2], sum = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int c = 2 * tid + k;
-        have[k] = c < n && plans[c].parts > 1 ? plans[c].rows * kSlices : 0;
-        sum += have[k];
-    }
-    int inc = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += v;
-    }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    int at = inc - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        if (w < warp) at += sums[w];
-        total += sums[w];
+    sm100::griddep_wait();
+    int have[2], inc[2];
+    {
+        Plan pl = {0, 0, 0, 0};
+        if (tid < n) list[tid] = pl = plans[tid];
+        have[0] = pl.parts > 1 && pl.parts <= kFewParts ? pl.rows : 0;
+        have[1] = pl.parts > kFewParts ? pl.rows * kSlices : 0;
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        if (2 * tid + k <= n) first[2 * tid + k] = at;
-        at += have[k];
+    for (int x = 0; x < 2; ++x) {
+        inc[x] = have[x];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc[x], d);
+            if (lane >= d) inc[x] += v;
+        }
+        if (lane == 31) sums[x][warp] = inc[x];
     }
     __syncthreads();
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        int lo = 0, hi = n;  // the last c with first[c] <= item
+    int total[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        int at = lane < kWarps ? sums[x][lane] : 0;
+        int before = lane < warp ? at : 0;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            at += __shfl_xor_sync(0xffffffffu, at, d);
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+        }
+        total[x] = at;
+        if (tid <= n) first[x][tid] = before + inc[x] - have[x];
+    }
+    __syncthreads();
+    auto find = [&](int x, int item) {  // the last c with first[x][c] <= item
+        int lo = 0, hi = n;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (first[mid] <= item) lo = mid; else hi = mid;
+            if (first[x][mid] <= item) lo = mid; else hi = mid;
         }
-        const int c = lo, r = (item - first[c]) / kSlices, ch = (item - first[c]) % kSlices * 64;
-        const Plan pl = plans[c];
-        auto part = [&](int k) { return parts + ((size_t)(c + k) * 2 + (k == 0)) * part_floats(D); };
-        // m over the parts, then mv relative to it
-        float m = -INFINITY, mv = -INFINITY;
-        for (int k = tid; k < pl.parts; k += 256) m = fmaxf(m, part(k)[4 * r]);
+        return lo;
+    };
+    auto part = [&](int c, int k) { return parts + ((size_t)(c + k) * 2 + (k == 0)) * part_floats(D); };
+    auto out_row = [&](const Plan &pl, int r) {
+        const int row = (pl.row_head >> 6) + r, head = pl.row_head & 63;
+        return p.out + ((size_t)(pl.row0 + row / G) * b.H + head * G + row % G) * D;
+    };
+
+    for (int item = warp * gridDim.x + blockIdx.x; item < total[0]; item += gridDim.x * kWarps) {
+        const int c = find(0, item), r = item - first[0][c];
+        const Plan pl = list[c];
+        const bool has = lane < pl.parts;  // at most 24: a lane holds one part's sums
+        const float4 st = has ? *reinterpret_cast<const float4 *>(part(c, lane) + 4 * r) : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        float4 v0[2][kVec];  // the first two parts, under the sums
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int x = 0; x < kVec; ++x)
+                v0[k][x] = (reinterpret_cast<const float4 *>(part(c, k) + 4 * kRowTile + r * D) + lane)[32 * x];
+        float m = st.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (lane == 0) red[warp][0] = m;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w][0]);
-        const float mz = finite_or_0(m);
-        for (int k = tid; k < pl.parts; k += 256) mv = fmaxf(mv, part(k)[4 * r + 1] + (part(k)[4 * r] - mz));
+        const float mz = finite_or_0(m), rel = st.y + (st.x - mz);
+        float mv = rel;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, d));
+        const float vz = finite_or_0(mv);
+        float l = has ? st.z * sm100::ex2_approx(st.x - mz) : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const float f = has ? sm100::ex2_approx(rel - vz) : 0.f;
+        float4 t[kVec];
+#pragma unroll
+        for (int x = 0; x < kVec; ++x) {
+            const float f0 = __shfl_sync(0xffffffffu, f, 0), f1 = __shfl_sync(0xffffffffu, f, 1);
+            t[x].x = v0[0][x].x * f0 + v0[1][x].x * f1, t[x].y = v0[0][x].y * f0 + v0[1][x].y * f1;
+            t[x].z = v0[0][x].z * f0 + v0[1][x].z * f1, t[x].w = v0[0][x].w * f0 + v0[1][x].w * f1;
+        }
+#pragma unroll 4
+        for (int k = 2; k < pl.parts; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float4 *src = reinterpret_cast<const float4 *>(part(c, k) + 4 * kRowTile + r * D) + lane;
+#pragma unroll
+            for (int x = 0; x < kVec; ++x) {
+                const float4 v = src[32 * x];
+                t[x].x += v.x * fk, t[x].y += v.y * fk, t[x].z += v.z * fk, t[x].w += v.w * fk;
+            }
+        }
+        const float g = l == 0.f ? 0.f : sm100::ex2_approx(vz) / l;
+        uint2 *dst = reinterpret_cast<uint2 *>(out_row(pl, r)) + lane;
+#pragma unroll
+        for (int x = 0; x < kVec; ++x)
+            dst[32 * x] = make_uint2(pack_bf16(t[x].x * g, t[x].y * g), pack_bf16(t[x].z * g, t[x].w * g));
+    }
+
+    for (int item = blockIdx.x; item < total[1]; item += gridDim.x) {
+        const int c = find(1, item), r = (item - first[1][c]) / kSlices, ch = (item - first[1][c]) % kSlices * 64;
+        const Plan pl = list[c];
+        // a half warp: every 64th part, four channels a lane; all loads before the sums
+        float4 v[kBatch], st[kBatch];
+        float m = -INFINITY, mv = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const int k = 2 * kWarps * x + 2 * warp + (lane >> 4);
+            const bool in = k < pl.parts;
+            st[x] = in ? *reinterpret_cast<const float4 *>(part(c, k) + 4 * r) : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+            v[x] = in ? *reinterpret_cast<const float4 *>(part(c, k) + 4 * kRowTile + r * D + ch + 4 * (lane & 15))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        // m over the parts, then mv relative to it
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) m = fmaxf(m, st[x].x);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (lane == 0) red[warp][0] = m;
+        __syncthreads();
+        m = lane < kWarps ? red[lane][0] : -INFINITY;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float mz = finite_or_0(m);
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) mv = fmaxf(mv, st[x].y + (st[x].x - mz));
+        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 16));
         if (lane == 0) red[warp][1] = mv;
         __syncthreads();
+        mv = lane < kWarps ? red[lane][1] : -INFINITY;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) mv = fmaxf(mv, red[w][1]);
+        for (int d = 16; d > 0; d >>= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, d));
         const float vz = finite_or_0(mv);
-        float l = 0.f;
-        float2 sum2 = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int k = warp; k < pl.parts; k += 8) {
-            const float4 st = *reinterpret_cast<const float4 *>(part(k) + 4 * r);
-            const float2 v = *reinterpret_cast<const float2 *>(part(k) + 4 * kRowTile + r * D + ch + 2 * lane);
-            const float f = sm100::ex2_approx(st.y + (st.x - mz) - vz);
-            l += st.z * sm100::ex2_approx(st.x - mz);
-            sum2.x += v.x * f, sum2.y += v.y * f;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const float f = sm100::ex2_approx(st[x].y + (st[x].x - mz) - vz);
+            l += st[x].z * sm100::ex2_approx(st[x].x - mz);
+            t.x += v[x].x * f, t.y += v[x].y * f, t.z += v[x].z * f, t.w += v[x].w * f;
         }
-        o[warp][lane] = sum2;
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, 16), t.y += __shfl_xor_sync(0xffffffffu, t.y, 16);
+        t.z += __shfl_xor_sync(0xffffffffu, t.z, 16), t.w += __shfl_xor_sync(0xffffffffu, t.w, 16);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (lane < 16) o[warp][lane] = t;
         if (lane == 0) red[warp][2] = l;
         __syncthreads();
-        if (warp == 0) {
+        if (tid < 16) {
             float lt = 0.f;
-            float2 t = make_float2(0.f, 0.f);
+            t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) lt += red[w][2], t.x += o[w][lane].x, t.y += o[w][lane].y;
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 x = o[w][tid];
+                lt += red[w][2], t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+            }
             const float f = lt == 0.f ? 0.f : sm100::ex2_approx(vz) / lt;
-            const Geometry g = geometry(p, pl.seq);
-            const int per_head = g.units / b.Hkv, row = pl.unit % per_head * kRowTile + r, head = pl.unit / per_head;
-            *reinterpret_cast<uint32_t *>(p.out + ((size_t)(g.row0 + row / G) * b.H + head * G + row % G) * D + ch + 2 * lane) =
-                pack_bf16(t.x * f, t.y * f);
+            reinterpret_cast<uint2 *>(out_row(pl, r) + ch)[tid] = make_uint2(pack_bf16(t.x * f, t.y * f), pack_bf16(t.z * f, t.w * f));
         }
         __syncthreads();
     }
+}
+
+// The pool as a matrix of codes [pages * Hkv * page_size, D]; a box is 128 channels of up to 64 slots of a page.
+bool encode_pool(CUtensorMap *m, const uint8_t *base, const Batch &b)
+{
+    const auto encode = encode_fn();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)b.D, (cuuint64_t)b.num_pages * b.Hkv * b.page}, strides[1] = {(cuuint64_t)b.D};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(b.page < kKeyTile ? b.page : kKeyTile)}, estride[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -649,10 +850,18 @@ rglru_status launch(const AttendArgs &p, cudaStream_t stream)
     const rglru_status st =
         set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_kernel<D>), C::kSmem, flag);
     if (st != RGLRU_OK) return st;
+    CUtensorMap tm_k, tm_v;
+    if (!encode_pool(&tm_k, p.k, p.b) || !encode_pool(&tm_v, p.v, p.b)) return RGLRU_ERR_CUDA;
     const int grid = kSms * C::kCtasPerSm;
-    rglru_paged_attention_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p);
-    rglru_paged_combine_kernel<D><<<kSms * 2, 256, 0, stream>>>(p, grid);
-    return cuda_status(cudaGetLastError());
+    rglru_paged_attention_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p, tm_k, tm_v);
+    if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSms), cfg.blockDim = dim3(kJoinThreads), cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, rglru_paged_combine_kernel<D>, p, grid));
 }
 
 }  // namespace
@@ -682,6 +891,7 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
     const size_t need = rglru_paged_attention_workspace_size(H, Hkv, head_dim);
     const rglru_status c = paged::check_batch(p.b, k_cache, k_scale, v_cache, v_scale, workspace_bytes, need);
     if (c != RGLRU_OK) return c;
+    if ((int64_t)num_pages * Hkv * page_size > INT32_MAX) return RGLRU_ERR_UNSUPPORTED;  // rows of a tensor map
     if (!args::al16(q) || !args::al16(out) || window < 1 || !(scale > 0.f) || scale > 1e30f) return RGLRU_ERR_INVALID_ARG;
     const size_t pool = (size_t)num_pages * Hkv, act = (size_t)rows * H * head_dim * 2;
     const args::Span in[] = {args::span(q, act),
