@@ -53,7 +53,6 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ float bf16_bits(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
 // eight nibbles to four bf16 pairs q - 8: (k0, k4), (k1, k5), (k2, k6), (k3, k7)
 __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4])
@@ -95,7 +94,35 @@ struct Few {
     static constexpr int kSmem = (kRingBytes > kSums ? kRingBytes : kSums) + 128;
 };
 
-template <int NT, int R, bool kE4m3>
+// Scales of a row at the sub-blocks of a block that end a group, as bf16 pairs (sub-blocks 0, 1 and 2, 3): one load where
+// the row's groups are a multiple of a block's (its address is aligned then), none for sub-blocks inside a group.
+template <bool kVec>
+__device__ __forceinline__ uint2 load_scales(const uint16_t *row, int k0, int K, int shift)
+{
+    if (row == nullptr) return make_uint2(0, 0);
+    const uint16_t *src = row + (k0 >> shift);
+    if (kVec) {
+        if (shift == 7) return make_uint2(0, (uint32_t)src[0] << 16);
+        if (shift == 5) return *reinterpret_cast<const uint2 *>(src);
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(src);
+        return make_uint2(v << 16, v & 0xffff0000u);
+    }
+    uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = k0 + 32 * i;
+        if (k < K && ((k + 32) & ((1 << shift) - 1)) == 0) v[i] = row[k >> shift];
+    }
+    return make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+}
+__device__ __forceinline__ float scale_at(uint2 v, int i)
+{
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+}
+
+// kVec: K is a multiple of 128 (then so are the scales' rows of a block's groups, and no block is cut)
+template <int NT, int R, bool kE4m3, bool kVec>
 __global__ void __launch_bounds__(kWarps * 32) rglru_linear_w4_kernel(const W4Args p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -104,121 +131,120 @@ __global__ void __launch_bounds__(kWarps * 32) rglru_linear_w4_kernel(const W4Ar
     const int n0 = blockIdx.x * 16 * R;
     const int blocks = (p.K + kBlockK - 1) / kBlockK;
     const int mine = blocks > warp ? (blocks - warp + kWarps - 1) / kWarps : 0;
-    const int groups = p.K >> p.group_shift;
+    const int groups = p.K >> p.group_shift, gmask = (1 << p.group_shift) - 1;
     uint8_t *ring = smem + warp * kRing * R * 1024;
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
 
-    auto load_w = [&](int b) {  // block b of this warp's
-        const int k0 = (warp + b * kWarps) * kBlockK;
+    // this lane's places: chunk j of its 2 R rows of W, its rows of x, its rows of scales; a warp's next block is kWarps on
+    const uint8_t *wp[2 * R];
+    const uint16_t *sp[2 * R];
+    uint32_t wdst[2 * R];
+#pragma unroll
+    for (int q = 0; q < 2 * R; ++q) {
+        const int r = q * 8 + quad, n = n0 + r;
+        wp[q] = n < p.N ? p.W + ((size_t)n * p.K + warp * kBlockK) / 2 + 16 * j : nullptr;
+        sp[q] = n < p.N ? p.W_scale + (size_t)n * groups : nullptr;
+        wdst[q] = (uint32_t)__cvta_generic_to_shared(ring) + r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
+    }
+    constexpr int kBytes = kE4m3 ? 1 : 2;
+    const uint8_t *xp[NT];
+    const float *asp[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int m = t * 8 + quad;
+        xp[t] = m < p.M ? static_cast<const uint8_t *>(p.A) + ((size_t)m * p.K + warp * kBlockK + 8 * j) * kBytes : nullptr;
+        asp[t] = kE4m3 && m < p.M ? p.A_scale + (size_t)m * (p.K >> p.a_shift) : nullptr;
+    }
+    auto load_w = [&](int b, int slot) {  // block b of this warp's
+        const bool in = kVec || (warp + b * kWarps) * kBlockK + 32 * j < p.K;
 #pragma unroll
         for (int q = 0; q < 2 * R; ++q) {
-            const int r = q * 8 + quad;  // row of the tile, chunk j
-            const bool in = n0 + r < p.N && k0 + 32 * j < p.K;
-            cp16(base + (b % kRing) * R * 1024 + r * 64 + ((j ^ ((r >> 1) & 3)) << 4),
-                 p.W + (in ? ((size_t)(n0 + r) * p.K + k0 + 32 * j) / 2 : 0), in);
+            const bool take = in && wp[q] != nullptr;
+            cp16(wdst[q] + slot * R * 1024, take ? wp[q] + (size_t)b * (kWarps * kBlockK / 2) : p.W, take);
         }
     };
-    uint4 xb[NT][4];      // bf16: 8 values a sub-block; e4m3: 8 codes in .x, .y and the scale in .z
-    uint16_t sb[R][2][4];
+    uint4 xb[NT][4];  // bf16: 8 values a sub-block; e4m3: 8 codes in .x, .y and the scale in .z
+    uint2 sb[2 * R];
     auto load_x = [&](int b) {
         const int k0 = (warp + b * kWarps) * kBlockK;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int m = t * 8 + quad;
+            const uint8_t *src = xp[t] + (size_t)b * (kWarps * kBlockK * kBytes);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int k = k0 + 32 * i + 8 * j;
                 xb[t][i] = make_uint4(0, 0, 0, 0);
-                if (m < p.M && k < p.K) {
+                if (xp[t] != nullptr && (kVec || k0 + 32 * i < p.K)) {
                     if (kE4m3) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.A) + (size_t)m * p.K + k);
-                        xb[t][i].x = v.x, xb[t][i].y = v.y;
-                        xb[t][i].z = __float_as_uint(p.A_scale[(size_t)m * (p.K >> p.a_shift) + (k >> p.a_shift)]);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(src + 32 * i);
+                        xb[t][i] = make_uint4(v.x, v.y, __float_as_uint(asp[t][(k0 + 32 * i) >> p.a_shift]), 0);
                     } else {
-                        xb[t][i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.A) + (size_t)m * p.K + k);
+                        xb[t][i] = *reinterpret_cast<const uint4 *>(src + 64 * i);
                     }
                 }
             }
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = n0 + 16 * r + 8 * h + quad;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = k0 + 32 * i;
-                    // a sub-block that ends its group needs the group's scale
-                    const bool ends = ((k + 32) & ((1 << p.group_shift) - 1)) == 0;
-                    sb[r][h][i] = n < p.N && k < p.K && ends ? p.W_scale[(size_t)n * groups + (k >> p.group_shift)] : (uint16_t)0;
-                }
-            }
+        for (int q = 0; q < 2 * R; ++q) sb[q] = load_scales<kVec>(sp[q], k0, p.K, p.group_shift);
     };
 
 #pragma unroll
     for (int b = 0; b < kRing - 1; ++b) {
-        if (b < mine) load_w(b);
+        if (b < mine) load_w(b, b);
         cp_commit();
     }
     if (mine > 0) load_x(0);
     float acc[R][NT][4] = {}, part[R][NT][4] = {};
     for (int b = 0; b < mine; ++b) {
         uint4 x[NT][4];
-        float s[R][2][4];
+        uint2 s[2 * R];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[t][i] = xb[t][i];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[r][h][i] = bf16_bits(sb[r][h][i]);
+        for (int q = 0; q < 2 * R; ++q) s[q] = sb[q];
         if (b + 1 < mine) load_x(b + 1);
         __syncwarp();  // the slot that is filled now was read a block ago
-        if (b + kRing - 1 < mine) load_w(b + kRing - 1);
+        if (b + kRing - 1 < mine) load_w(b + kRing - 1, (b + kRing - 1) % kRing);
         cp_commit();
         cp_wait<kRing - 1>();
         __syncwarp();
-        const uint8_t *w = ring + (b % kRing) * R * 1024;
+        const uint8_t *w = ring + (b % kRing) * R * 1024 + quad * 64 + 4 * j;
         const int k0 = (warp + b * kWarps) * kBlockK;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (k0 + 32 * i >= p.K) break;
-            const bool begins = ((k0 + 32 * i) & ((1 << p.group_shift) - 1)) == 0;
-            uint32_t xp[NT][4];
+            if (!kVec && k0 + 32 * i >= p.K) break;
+            const bool begins = ((32 * i + (kVec ? 0 : k0)) & gmask) == 0, ends = ((32 * i + 32 + (kVec ? 0 : k0)) & gmask) == 0;
+            uint32_t xq[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (kE4m3)
-                    pair_up_e4m3(make_uint2(x[t][i].x, x[t][i].y), __uint_as_float(x[t][i].z), xp[t]);
+                    pair_up_e4m3(make_uint2(x[t][i].x, x[t][i].y), __uint_as_float(x[t][i].z), xq[t]);
                 else
-                    pair_up(x[t][i], xp[t]);
+                    pair_up(x[t][i], xq[t]);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int sw = ((i ^ (quad >> 1)) << 4) + 4 * j;  // rows quad and quad + 8 share the swizzle
+                const int sw = (i ^ (quad >> 1)) << 4;  // rows quad and quad + 8 share the swizzle
                 uint32_t lo[4], hi[4];
-                unpack(*reinterpret_cast<const uint32_t *>(w + (16 * r + quad) * 64 + sw), lo);
-                unpack(*reinterpret_cast<const uint32_t *>(w + (16 * r + quad + 8) * 64 + sw), hi);
+                unpack(*reinterpret_cast<const uint32_t *>(w + r * 1024 + sw), lo);
+                unpack(*reinterpret_cast<const uint32_t *>(w + r * 1024 + 512 + sw), hi);
                 const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+                if (begins) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (begins)
-                        mma_bf16_first(part[r][t], a0, xp[t][0], xp[t][1]);
-                    else
-                        mma_bf16(part[r][t], a0, xp[t][0], xp[t][1]);
-                    mma_bf16(part[r][t], a1, xp[t][2], xp[t][3]);
+                    for (int t = 0; t < NT; ++t) mma_bf16_first(part[r][t], a0, xq[t][0], xq[t][1]);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_bf16(part[r][t], a0, xq[t][0], xq[t][1]);
                 }
-            }
-            if (((k0 + 32 * i + 32) & ((1 << p.group_shift) - 1)) == 0) {  // the group ends here
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int t = 0; t < NT; ++t) mma_bf16(part[r][t], a1, xq[t][2], xq[t][3]);
+                if (ends) {
+                    const float s0 = scale_at(s[2 * r], i), s1 = scale_at(s[2 * r + 1], i);
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[r][t][e] = fmaf(part[r][t][e], s[r][e >> 1][i], acc[r][t][e]);
+                        for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(part[r][t][e], e < 2 ? s0 : s1, acc[r][t][e]);
+                }
             }
         }
     }
@@ -245,19 +271,22 @@ __global__ void __launch_bounds__(kWarps * 32) rglru_linear_w4_kernel(const W4Ar
 }
 
 // ------------------------------------------------------------------------------------------------ 17 to 64 rows
-// A CTA takes 128 outputs (8 warps of 16) over its share of K's blocks, x is shared by its warps: its block comes by
-// cp.async, is paired (and taken out of e4m3) once per CTA a block ahead, and then read as whole operands.  CTAs of a
-// cluster share the outputs and split K; their sums meet through distributed shared memory.
+// K is split over the CTAs of a cluster, so that a CTA holds its share of x in shared memory as finished operands (paired, and
+// taken out of e4m3, once) while it walks over the outputs: a round is 128 of them, 16 a warp, and no warp waits for another
+// within it.  A warp's weights come by cp.async into its own ring, across rounds, its scales into registers one block ahead.  At a
+// round's end the cluster's sums meet through distributed shared memory, in rank order.
+// With x re-read for every 128 outputs instead (a barrier and a conversion each block) 37 rows of
+// 12289 x 4096 took 68 us.
 constexpr int kWideThreads = 256, kWideN = 128, kWideRing = 4;
 
 template <int NT>
 struct Wide {
-    static constexpr int kW = kWideN * 64;            // weights of a block
-    static constexpr int kX = 8 * NT * kBlockK * 2;   // x of a block: as it comes (bf16; e4m3 half of it), and paired
-    static constexpr int kStage = kW + kX;
-    static constexpr int kSums = kWideN * (8 * NT + 1) * 4;
-    static constexpr int kLoop = kWideRing * kStage + 2 * kX + 2 * 4 * kWideN * 4;
-    static constexpr int kSmem = (kLoop > kSums ? kLoop : kSums) + 128;
+    static constexpr int kX = 8 * NT * kBlockK * 2;  // operands of a block
+    static constexpr int kRingBytes = kWarps * kWideRing * 1024;
+    // sums of two rounds: [2][128 outputs][M, made odd]
+    static constexpr int sums(int M) { return 2 * kWideN * (M | 1) * 4; }
+    static constexpr int smem(int blocks, int M) { return blocks * kX + kRingBytes + sums(M) + 128; }
+    static constexpr int max_blocks(int M) { return (226 * 1024 - kRingBytes - sums(M) - 128) / kX; }
 };
 
 // the same shared-memory place in CTA `rank` of the cluster
@@ -268,203 +297,262 @@ __device__ __forceinline__ const float *peer(const float *x, int rank)
     return reinterpret_cast<const float *>(a);
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kWideThreads, 2) rglru_linear_w4_wide_kernel(const W4Args p, int cluster)
+// kShift: log2 of the group where K is a multiple of 128, or 0: any group, any K.  held: blocks of x in shared memory at a
+// time.
+template <int NT, int kShift>
+__global__ void __launch_bounds__(kWideThreads, 2) rglru_linear_w4_wide_kernel(const W4Args p, int cluster, int held)
 {
     using C = Wide<NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    uint8_t *paired = smem + kWideRing * C::kStage;
-    float *scales = reinterpret_cast<float *>(paired + 2 * C::kX);  // [2][4 sub-blocks][128 rows]
+    uint4 *xs = reinterpret_cast<uint4 *>(smem);  // [block][sub-block][row of x][thread of a quad]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, j = lane & 3;
-    const int srow = tid & (kWideN - 1), shalf = tid / kWideN;  // whose scales this thread loads: row, sub-block pair
-    const int rank = (int)(blockIdx.x % cluster), n0 = (int)(blockIdx.x / cluster) * kWideN;
-    const int blocks = (p.K + kBlockK - 1) / kBlockK;
+    uint8_t *ring = smem + held * C::kX + warp * kWideRing * 1024;
+    float *sums = reinterpret_cast<float *>(smem + held * C::kX + C::kRingBytes);  // [2][128 outputs][sum_row]
+    const int rank = (int)(blockIdx.x % cluster), first = (int)(blockIdx.x / cluster), step = (int)(gridDim.x / cluster);
+    const int tiles = (p.N + kWideN - 1) / kWideN, blocks = (p.K + kBlockK - 1) / kBlockK;
     const int b0 = (int)((long long)blocks * rank / cluster), count = (int)((long long)blocks * (rank + 1) / cluster) - b0;
-    const int groups = p.K >> p.group_shift, gmask = (1 << p.group_shift) - 1;
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-    const bool e4 = p.A_scale != nullptr;
+    constexpr bool kVec = kShift != 0;
+    const int shift = kVec ? kShift : p.group_shift, groups = p.K >> shift, gmask = (1 << shift) - 1, sum_row = p.M | 1;
+    const int rounds = (tiles - first + step - 1) / step;  // at least one: the grid has no more clusters than tiles
+    const uint32_t wdst = (uint32_t)__cvta_generic_to_shared(ring) + quad * 64 + ((j ^ (quad >> 1)) << 4);
 
-    auto load = [&](int b) {
-        const int k0 = (b0 + b) * kBlockK;
-        const uint32_t st = base + (b % kWideRing) * C::kStage;
+    auto load_x = [&](int b, int n) {  // blocks b .. b + n - 1 of this rank's into xs
+        constexpr int kBatch = 4;  // loads in flight a thread
+        const int all = n * 8 * NT * 16;
+        for (int c0 = tid; c0 < all; c0 += kBatch * kWideThreads) {
+            uint4 v[kBatch];
+            float sc[kBatch];
 #pragma unroll
-        for (int q = 0; q < kWideN * 4 / kWideThreads; ++q) {
-            const int r = q * (kWideThreads / 4) + (tid >> 2), i = tid & 3;
-            const bool in = n0 + r < p.N && k0 + 32 * i < p.K;
-            cp16(st + r * 64 + ((i ^ ((r >> 1) & 3)) << 4), p.W + (in ? ((size_t)(n0 + r) * p.K + k0 + 32 * i) / 2 : 0), in);
-        }
-        const int per = e4 ? 8 : 16, bytes = e4 ? 1 : 2;  // 16-byte chunks of a row of x
-        for (int c = tid; c < 8 * NT * per; c += kWideThreads) {
-            const int m = c / per, k = k0 + c % per * (16 / bytes);
-            const bool in = m < p.M && k < p.K;
-            cp16(st + C::kW + c * 16, static_cast<const uint8_t *>(p.A) + (in ? ((size_t)m * p.K + k) * bytes : 0), in);
-        }
-    };
-    // x of block b, from its stage to operands: [sub-block][row][j] of 16 bytes, the 4 threads of a quad side by side
-    auto convert = [&](int b) {
-        const uint8_t *src = smem + (b % kWideRing) * C::kStage + C::kW;
-        uint4 *dst = reinterpret_cast<uint4 *>(paired + (b & 1) * C::kX);
-#pragma unroll
-        for (int q = 0; q < (8 * NT * 16 + kWideThreads - 1) / kWideThreads; ++q) {
-            const int c = q * kWideThreads + tid, m = c >> 4, o = c & 15;  // octet o of row m: sub-block o / 4, thread o % 4
-            if (c >= 8 * NT * 16) break;
-            uint32_t r[4];
-            if (e4) {
-                const int k = (b0 + b) * kBlockK + 8 * o;
-                const float s = m < p.M && k < p.K ? p.A_scale[(size_t)m * (p.K >> p.a_shift) + (k >> p.a_shift)] : 0.f;
-                pair_up_e4m3(*reinterpret_cast<const uint2 *>(src + c * 8), s, r);
-            } else {
-                pair_up(*reinterpret_cast<const uint4 *>(src + c * 16), r);
+            for (int u = 0; u < kBatch; ++u) {
+                const int c = c0 + u * kWideThreads, o = c & 15, m = (c >> 4) % (8 * NT);  // octet o of row m
+                const int k = (b0 + b + c / (8 * NT * 16)) * kBlockK + 8 * o;
+                v[u] = make_uint4(0, 0, 0, 0);
+                sc[u] = 0.f;
+                if (c < all && m < p.M && k < p.K) {
+                    if (p.A_scale != nullptr) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.A) + (size_t)m * p.K + k);
+                        v[u].x = w.x, v[u].y = w.y;
+                        sc[u] = p.A_scale[(size_t)m * (p.K >> p.a_shift) + (k >> p.a_shift)];
+                    } else {
+                        v[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.A) + (size_t)m * p.K + k);
+                    }
+                }
             }
-            dst[(o >> 2) * 32 * NT + m * 4 + (o & 3)] = make_uint4(r[0], r[1], r[2], r[3]);
-        }
-    };
-    // the scales of a block, at the sub-blocks that end a group
-    uint16_t sc[2];
-    auto load_scales = [&](int b) {
-        const uint16_t *src = p.W_scale + (size_t)(n0 + srow) * groups;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = (b0 + b) * kBlockK + 64 * shalf + 32 * i;
-            sc[i] = n0 + srow < p.N && k < p.K && ((k + 32) & gmask) == 0 ? src[k >> p.group_shift] : (uint16_t)0;
+            for (int u = 0; u < kBatch; ++u) {
+                const int c = c0 + u * kWideThreads, o = c & 15, m = (c >> 4) % (8 * NT), x = c / (8 * NT * 16);
+                uint32_t r[4];
+                if (p.A_scale != nullptr)
+                    pair_up_e4m3(make_uint2(v[u].x, v[u].y), sc[u], r);
+                else
+                    pair_up(v[u], r);
+                if (c < all) xs[(x * 4 + (o >> 2)) * 32 * NT + m * 4 + (o & 3)] = make_uint4(r[0], r[1], r[2], r[3]);
+            }
         }
-    };
-    auto store_scales = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) scales[((b & 1) * 4 + 2 * shalf + i) * kWideN + srow] = bf16_bits(sc[i]);
     };
 
+    // A warp's line of blocks, over all rounds; the weights are kRing - 1 blocks ahead, the scales one.  Rows quad and
+    // quad + 8 of the warp's 16: chunk j of their weights, their scales.
+    struct Ahead {
+        int round, b;
+        const uint8_t *w[2];
+        const uint16_t *s[2];
+    };
+    auto place = [&](Ahead &a) {
 #pragma unroll
-    for (int b = 0; b < kWideRing - 1; ++b) {
-        if (b < count) load(b);
+        for (int h = 0; h < 2; ++h) {
+            const int n = (first + a.round * step) * kWideN + warp * 16 + 8 * h + quad;
+            a.w[h] = n < p.N ? p.W + ((size_t)n * p.K + b0 * kBlockK) / 2 + 16 * j : nullptr;
+            a.s[h] = n < p.N ? p.W_scale + (size_t)n * groups : nullptr;
+        }
+    };
+    Ahead aw = {0, 0, {}, {}}, as = {0, 0, {}, {}};
+    place(aw), place(as);
+    int ld_slot = 0, slot = 0;
+    uint2 sb[2] = {};
+    auto load_w = [&]() {
+        if (aw.round < rounds) {
+            const bool in = kVec || (b0 + aw.b) * kBlockK + 32 * j < p.K;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool take = in && aw.w[h] != nullptr;
+                cp16(wdst + ld_slot * 1024 + 512 * h, take ? aw.w[h] + aw.b * (kBlockK / 2) : p.W, take);
+            }
+            if (++ld_slot == kWideRing) ld_slot = 0;
+            if (++aw.b == count) aw.b = 0, ++aw.round, place(aw);
+        }
         cp_commit();
-    }
-    float acc[NT][4] = {}, part[NT][4] = {};
+    };
+    auto load_s = [&]() {
+        if (as.round < rounds) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) sb[h] = load_scales<kVec>(as.s[h], (b0 + as.b) * kBlockK, p.K, shift);
+            if (++as.b == count) as.b = 0, ++as.round, place(as);
+        }
+    };
     if (count > 0) {
-        load_scales(0);
-        cp_wait<kWideRing - 2>();
-        __syncthreads();
-        convert(0);
-        store_scales(0);
-        if (count > 1) load_scales(1);
+#pragma unroll
+        for (int b = 0; b < kWideRing - 1; ++b) load_w();
+        load_s();
     }
-    for (int b = 0; b < count; ++b) {
-        cp_wait<kWideRing - 3>();
-        __syncthreads();  // block b is paired, block b + 1 has landed, block b - 1 is done with
-        if (b + kWideRing - 1 < count) load(b + kWideRing - 1);
-        cp_commit();
-        if (b + 1 < count) {
-            convert(b + 1);
-            store_scales(b + 1);
-            if (b + 2 < count) load_scales(b + 2);
-        }
-        const uint8_t *w = smem + (b % kWideRing) * C::kStage;
-        const uint4 *xs = reinterpret_cast<const uint4 *>(paired + (b & 1) * C::kX);
-        const float *s = scales + (b & 1) * 4 * kWideN + warp * 16 + quad;
-        const int k0 = (b0 + b) * kBlockK;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (k0 + 32 * i >= p.K) break;
-            const bool begins = ((k0 + 32 * i) & gmask) == 0;
-            const int sw = ((i ^ (quad >> 1)) << 4) + 4 * j;
-            uint32_t lo[4], hi[4];
-            unpack(*reinterpret_cast<const uint32_t *>(w + (warp * 16 + quad) * 64 + sw), lo);
-            unpack(*reinterpret_cast<const uint32_t *>(w + (warp * 16 + quad + 8) * 64 + sw), hi);
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-            if (begins) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint4 x = xs[i * 32 * NT + t * 32 + lane];
-                    mma_bf16_first(part[t], a0, x.x, x.y);
-                    mma_bf16(part[t], a1, x.z, x.w);
-                }
-            } else {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint4 x = xs[i * 32 * NT + t * 32 + lane];
-                    mma_bf16(part[t], a0, x.x, x.y);
-                    mma_bf16(part[t], a1, x.z, x.w);
-                }
-            }
-            if (((k0 + 32 * i + 32) & gmask) == 0) {
-                const float s0 = s[i * kWideN], s1 = s[i * kWideN + 8];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(part[t][e], e < 2 ? s0 : s1, acc[t][e]);
-            }
-        }
-    }
-    cp_wait<0>();
-    __syncthreads();
-    float *sums = reinterpret_cast<float *>(smem);  // [128 outputs][8 NT + 1], over the ring
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            sums[(warp * 16 + 8 * (e >> 1) + quad) * (8 * NT + 1) + 8 * t + 2 * j + (e & 1)] = acc[t][e];
-    sm100::cluster_sync();
-    // this CTA's outputs of the cluster's, summed in rank order
-    const int r0 = kWideN * rank / cluster, share = kWideN * (rank + 1) / cluster - r0;
-    for (int i = tid; i < share * p.M; i += kWideThreads) {
-        const int r = r0 + i % share, m = i / share, n = n0 + r;
-        if (n >= p.N) continue;
-        float v = 0.f;
+    // this CTA's outputs of the cluster's, of one round
+    auto join = [&](int round) {
+        const int n0 = (first + round * step) * kWideN, r0 = kWideN * rank / cluster;
+        const int share = kWideN * (rank + 1) / cluster - r0;
+        const float *from = sums + (round & 1) * kWideN * sum_row;
+        for (int i = tid; i < share * p.M; i += kWideThreads) {
+            const int r = r0 + i % share, m = i / share, n = n0 + r;
+            if (n >= p.N) continue;
+            float v = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < cluster; ++c) v += *peer(sums + r * (8 * NT + 1) + m, c);
-        p.out[(size_t)m * p.N + n] = __float2bfloat16_rn(v + (p.bias != nullptr ? p.bias[n] : 0.f));
+            for (int c = 0; c < cluster; ++c) v += *peer(from + r * sum_row + m, c);
+            p.out[(size_t)m * p.N + n] = __float2bfloat16_rn(v + (p.bias != nullptr ? p.bias[n] : 0.f));
+        }
+        __syncwarp();
+    };
+    const bool once = count <= held;
+    if (once) {
+        load_x(0, count);
+        __syncthreads();
     }
+    for (int round = 0; round < rounds; ++round) {
+        float acc[NT][4] = {}, part[NT][4] = {};
+        for (int b = 0; b < count; ++b) {
+            if (!once && b % held == 0) {
+                __syncthreads();
+                load_x(b, min(held, count - b));
+                __syncthreads();
+            }
+            const uint2 s[2] = {sb[0], sb[1]};
+            load_s();
+            __syncwarp();  // the slot that is filled now was read a block ago
+            load_w();
+            cp_wait<kWideRing - 1>();
+            __syncwarp();
+            const uint8_t *w = ring + slot * 1024 + quad * 64 + 4 * j;
+            if (++slot == kWideRing) slot = 0;
+            const uint4 *xb = xs + (once ? b : b % held) * 4 * 32 * NT + lane;
+            const int k0 = (b0 + b) * kBlockK;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!kVec && k0 + 32 * i >= p.K) break;
+                const int sw = (i ^ (quad >> 1)) << 4;
+                uint32_t lo[4], hi[4];
+                unpack(*reinterpret_cast<const uint32_t *>(w + sw), lo);
+                unpack(*reinterpret_cast<const uint32_t *>(w + 512 + sw), hi);
+                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+                uint4 x[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) x[t] = xb[(i * NT + t) * 32];
+                if (((32 * i + (kVec ? 0 : k0)) & gmask) == 0) {  // a group begins
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_bf16_first(part[t], a0, x[t].x, x[t].y);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_bf16(part[t], a0, x[t].x, x[t].y);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma_bf16(part[t], a1, x[t].z, x[t].w);
+                if (((32 * i + 32 + (kVec ? 0 : k0)) & gmask) == 0) {
+                    const float s0 = scale_at(s[0], i), s1 = scale_at(s[1], i);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(part[t][e], e < 2 ? s0 : s1, acc[t][e]);
+                }
+            }
+        }
+        // the last round's sums meet now that a round's work has passed since they were written
+        if (round > 0) {
+            sm100::cluster_wait();
+            join(round - 1);
+        }
+        float *mine = sums + (round & 1) * kWideN * sum_row;  // all have read what was here: that was before they arrived
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (8 * t + 2 * j + (e & 1) < p.M)
+                    mine[(warp * 16 + 8 * (e >> 1) + quad) * sum_row + 8 * t + 2 * j + (e & 1)] = acc[t][e];
+        __syncwarp();
+        sm100::cluster_arrive();
+    }
+    sm100::cluster_wait();
+    join(rounds - 1);
+    cp_wait<0>();
+    __syncwarp();
     sm100::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 constexpr int kSms = 148;
 
-template <int NT, int R, bool kE4m3>
+template <int NT, int R, bool kE4m3, bool kVec>
 rglru_status launch_few(const W4Args &p, cudaStream_t stream)
 {
     using C = Few<NT, R>;
     static PerDeviceFlag flag;
     const rglru_status st =
-        set_smem_limit_once(reinterpret_cast<const void *>(rglru_linear_w4_kernel<NT, R, kE4m3>), C::kSmem, flag);
+        set_smem_limit_once(reinterpret_cast<const void *>(rglru_linear_w4_kernel<NT, R, kE4m3, kVec>), C::kSmem, flag);
     if (st != RGLRU_OK) return st;
-    rglru_linear_w4_kernel<NT, R, kE4m3><<<(unsigned)((p.N + 16 * R - 1) / (16 * R)), kWarps * 32, C::kSmem, stream>>>(p);
+    rglru_linear_w4_kernel<NT, R, kE4m3, kVec>
+        <<<(unsigned)((p.N + 16 * R - 1) / (16 * R)), kWarps * 32, C::kSmem, stream>>>(p);
     return cuda_status(cudaGetLastError());
+}
+template <int NT, int R>
+rglru_status launch_few(const W4Args &p, cudaStream_t stream)
+{
+    const bool vec = p.K % kBlockK == 0;
+    if (p.A_scale != nullptr) return vec ? launch_few<NT, R, true, true>(p, stream) : launch_few<NT, R, true, false>(p, stream);
+    return vec ? launch_few<NT, R, false, true>(p, stream) : launch_few<NT, R, false, false>(p, stream);
 }
 template <int NT>
 rglru_status launch_few(const W4Args &p, cudaStream_t stream)
 {
     // two row tiles a CTA read x half as often, once that leaves a CTA for every SM
-    if (p.N > 32 * kSms)
-        return p.A_scale != nullptr ? launch_few<NT, 2, true>(p, stream) : launch_few<NT, 2, false>(p, stream);
-    return p.A_scale != nullptr ? launch_few<NT, 1, true>(p, stream) : launch_few<NT, 1, false>(p, stream);
+    return p.N > 32 * kSms ? launch_few<NT, 2>(p, stream) : launch_few<NT, 1>(p, stream);
 }
 
-template <int NT>
+template <int NT, int kShift>
 rglru_status launch_wide(const W4Args &p, cudaStream_t stream)
 {
     using C = Wide<NT>;
-    static PerDeviceFlag flag;
-    const rglru_status st =
-        set_smem_limit_once(reinterpret_cast<const void *>(rglru_linear_w4_wide_kernel<NT>), C::kSmem, flag);
-    if (st != RGLRU_OK) return st;
-    // K is split so that the busiest SM has the least to do: its CTAs times a CTA's blocks and about two blocks' time
-    // to begin and end one
-    const int tiles = (p.N + kWideN - 1) / kWideN, blocks = (p.K + kBlockK - 1) / kBlockK;
-    int cluster = 1;
+    // The split of K: rounds of the busiest SM times a round's blocks (and about two blocks' time to end it), over
+    // cluster sizes; two CTAs on an SM share its issue slots, but hide each other's latency (three quarters of the time).
+    // Clusters of several CTAs find room on 132 of the 148 SMs (33 clusters of 4 were resident, the rest of a GPC
+    // does not hold one): one cluster more would run after all others.
+    const int tiles = (p.N + kWideN - 1) / kWideN, blocks = (p.K + kBlockK - 1) / kBlockK, most = C::max_blocks(p.M);
+    int cluster = 1, clusters = 1, held = 1;
     long long best = -1;
-    for (int c = 1; c <= 8; ++c) {
-        const long long cost = (((long long)tiles * c + kSms - 1) / kSms) * ((blocks + c - 1) / c + 2);
-        if (best < 0 || cost < best) best = cost, cluster = c;
+    for (int c = 1; c <= 8; c *= 2) {
+        const int share = (blocks + c - 1) / c, h = share < most ? share : most;
+        const int per_sm = C::smem(h, p.M) <= 113 * 1024 ? 2 : 1;
+        int n = (c == 1 ? kSms : 132) * per_sm / c;
+        if (n > tiles) n = tiles;
+        const int busy = n * c > kSms ? 6 : 4;  // CTAs that share an SM
+        const long long cost = ((long long)(tiles + n - 1) / n) * (share + 2 + (share > h ? share : 0)) * busy;
+        if (best < 0 || cost < best) best = cost, cluster = c, clusters = n, held = h;
     }
+    static PerDeviceFlag flag;
+    const rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_linear_w4_wide_kernel<NT, kShift>),
+                                                227 * 1024, flag);
+    if (st != RGLRU_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * cluster)), cfg.blockDim = dim3(kWideThreads), cfg.stream = stream;
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.gridDim = dim3((unsigned)(clusters * cluster)), cfg.blockDim = dim3(kWideThreads), cfg.stream = stream;
+    cfg.dynamicSmemBytes = C::smem(held, p.M);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)cluster, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
     cfg.attrs = &attr, cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, rglru_linear_w4_wide_kernel<NT>, p, cluster));
+    return cuda_status(cudaLaunchKernelEx(&cfg, rglru_linear_w4_wide_kernel<NT, kShift>, p, cluster, held));
+}
+template <int NT>
+rglru_status launch_wide(const W4Args &p, cudaStream_t stream)
+{
+    if (p.K % kBlockK != 0) return launch_wide<NT, 0>(p, stream);
+    return p.group_shift == 5   ? launch_wide<NT, 5>(p, stream)
+           : p.group_shift == 6 ? launch_wide<NT, 6>(p, stream)
+                                : launch_wide<NT, 7>(p, stream);
 }
 
 }  // namespace
@@ -497,11 +585,10 @@ extern "C" RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group
     switch ((M + 7) / 8) {
     case 1: return launch_few<1>(p, stream);
     case 2: return launch_few<2>(p, stream);
-    case 3: return launch_wide<3>(p, stream);
+    case 3:
     case 4: return launch_wide<4>(p, stream);
     case 5: return launch_wide<5>(p, stream);
     case 6: return launch_wide<6>(p, stream);
-    case 7: return launch_wide<7>(p, stream);
     default: return launch_wide<8>(p, stream);
     }
 }
