@@ -860,15 +860,24 @@ E4M3 = torch.float8_e4m3fn
 FULL_WINDOW = 1 << 30  # a window that reaches every position
 
 
+def _need(t, name: str, shape: tuple, dtype, dev) -> None:
+    """_check for calls that are made for every token: one expression when all is well, the
+    message from _check otherwise."""
+    if not (type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.device == dev
+            and t.is_contiguous()):
+        _check(t, name, shape, dtype, dev)
+
+
 def _enqueue(name: str, dev: torch.device, *args) -> None:
     """Runs the library call ``name`` on ``dev`` (made current for the launch) and its current stream."""
-    stream = _stream(dev)
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be CUDA tensors, got device {dev}")
     fn = getattr(_lib or load(), name)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if st != OK:
         raise RGLRUError(st, name)
 
@@ -882,13 +891,13 @@ def _norm_args(x, residual, weight, residual_out):
     if N == 0 or x.numel() == 0:
         raise ValueError("x must be [..., N] with at least one row")
     dev = x.device
-    _check(x, "x", x.shape, torch.bfloat16, dev)
-    _check(weight, "weight", (N,), torch.float32, dev)
+    _need(x, "x", x.shape, torch.bfloat16, dev)
+    _need(weight, "weight", (N,), torch.float32, dev)
     if residual is not None:
-        _check(residual, "residual", x.shape, torch.bfloat16, dev)
+        _need(residual, "residual", x.shape, torch.bfloat16, dev)
         if residual_out is None:
             residual_out = torch.empty_like(x)
-        _check(residual_out, "residual_out", x.shape, torch.bfloat16, dev)
+        _need(residual_out, "residual_out", x.shape, torch.bfloat16, dev)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     return x.numel() // N, N, dev, residual_out
@@ -900,7 +909,7 @@ def add_rmsnorm(x, residual, weight, eps: float = 1e-6, out=None, residual_out=N
     M, N, dev, residual_out = _norm_args(x, residual, weight, residual_out)
     if out is None:
         out = torch.empty_like(x)
-    _check(out, "out", x.shape, torch.bfloat16, dev)
+    _need(out, "out", x.shape, torch.bfloat16, dev)
     _enqueue("rglru_add_rmsnorm", dev, M, N, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
              _addr(residual_out), out.data_ptr())
     return out, (x if residual is None else residual_out)
@@ -915,11 +924,11 @@ def add_rmsnorm_e4m3(x, residual, weight, eps: float = 1e-6, group: int = 128, o
         raise ValueError(f"N = {N} is not a multiple of group = {group}")
     if out is None:
         out = torch.empty(x.shape, dtype=E4M3, device=dev)
-    _check(out, "out", x.shape, E4M3, dev)
+    _need(out, "out", x.shape, E4M3, dev)
     shape = (*x.shape[:-1], N // group)
     if scale is None:
         scale = torch.empty(shape, dtype=torch.float32, device=dev)
-    _check(scale, "scale", shape, torch.float32, dev)
+    _need(scale, "scale", shape, torch.float32, dev)
     _enqueue("rglru_add_rmsnorm_e4m3", dev, M, N, group, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
              _addr(residual_out), out.data_ptr(), scale.data_ptr())
     return out, scale, (x if residual is None else residual_out)
@@ -934,24 +943,24 @@ def linear_w4(A, W, W_scale, bias=None, A_scale=None, out=None) -> torch.Tensor:
     M, K = A.shape
     N = W.shape[0]
     dev = A.device
-    _check(A, "A", (M, K), torch.bfloat16 if A_scale is None else E4M3, dev)
-    _check(W, "W", (N, K // 2), torch.uint8, dev)
+    _need(A, "A", (M, K), torch.bfloat16 if A_scale is None else E4M3, dev)
+    _need(W, "W", (N, K // 2), torch.uint8, dev)
     G = W_scale.shape[1]
     if M == 0 or N == 0 or G == 0 or K == 0 or K % G != 0:
         raise ValueError(f"W_scale: {G} groups do not divide K = {K}, or a size is zero")
-    _check(W_scale, "W_scale", (N, G), torch.bfloat16, dev)
+    _need(W_scale, "W_scale", (N, G), torch.bfloat16, dev)
     a_group = 0
     if A_scale is not None:
         GA = A_scale.shape[1]
         if GA == 0 or K % GA != 0:
             raise ValueError(f"A_scale: {GA} groups do not divide K = {K}")
-        _check(A_scale, "A_scale", (M, GA), torch.float32, dev)
+        _need(A_scale, "A_scale", (M, GA), torch.float32, dev)
         a_group = K // GA
     if bias is not None:
-        _check(bias, "bias", (N,), torch.float32, dev)
+        _need(bias, "bias", (N,), torch.float32, dev)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    _check(out, "out", (M, N), torch.bfloat16, dev)
+    _need(out, "out", (M, N), torch.bfloat16, dev)
     _enqueue("rglru_linear_w4", dev, M, N, K, K // G, A.data_ptr(), _addr(A_scale), a_group, W.data_ptr(),
              W_scale.data_ptr(), _addr(bias), out.data_ptr())
     return out
@@ -991,17 +1000,17 @@ def _paged_args(batch: PagedBatch, cache: PagedCache, dev):
     if cache.k.dim() != 4:
         raise ValueError("cache.k must be [pages, Hkv, page_size, D]")
     P, Hkv, ps, D = shape = tuple(cache.k.shape)
-    _check(cache.k, "cache.k", shape, E4M3, dev)
-    _check(cache.v, "cache.v", shape, E4M3, dev)
-    _check(cache.k_scale, "cache.k_scale", (P, Hkv), torch.float32, dev)
-    _check(cache.v_scale, "cache.v_scale", (P, Hkv), torch.float32, dev)
+    _need(cache.k, "cache.k", shape, E4M3, dev)
+    _need(cache.v, "cache.v", shape, E4M3, dev)
+    _need(cache.k_scale, "cache.k_scale", (P, Hkv), torch.float32, dev)
+    _need(cache.v_scale, "cache.v_scale", (P, Hkv), torch.float32, dev)
     if batch.ctx_len.dim() != 1 or batch.block_table.dim() != 2:
         raise ValueError("ctx_len must be [S] and block_table [S, max_pages]")
     S = batch.ctx_len.shape[0]
     max_pages = batch.block_table.shape[1]
-    _check(batch.cu_tokens, "cu_tokens", (S + 1,), torch.int32, dev)
-    _check(batch.ctx_len, "ctx_len", (S,), torch.int32, dev)
-    _check(batch.block_table, "block_table", (S, max_pages), torch.int32, dev)
+    _need(batch.cu_tokens, "cu_tokens", (S + 1,), torch.int32, dev)
+    _need(batch.ctx_len, "ctx_len", (S,), torch.int32, dev)
+    _need(batch.block_table, "block_table", (S, max_pages), torch.int32, dev)
     return S, Hkv, D, ps, P, max_pages
 
 
@@ -1024,10 +1033,10 @@ def paged_append(qkv, batch: PagedBatch, cache: PagedCache, rope_base: float = 1
     if H < 1:
         raise ValueError("qkv must be [rows, (H + 2 Hkv) * D] with at least one query head")
     rows = qkv.shape[0]
-    _check(qkv, "qkv", (rows, (H + 2 * Hkv) * D), torch.bfloat16, dev)
+    _need(qkv, "qkv", (rows, (H + 2 * Hkv) * D), torch.bfloat16, dev)
     if q_out is None:
         q_out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
-    _check(q_out, "q_out", (rows, H * D), torch.bfloat16, dev)
+    _need(q_out, "q_out", (rows, H * D), torch.bfloat16, dev)
     workspace, nb = _paged_workspace(workspace, 4096, dev)
     _enqueue("rglru_paged_append", dev, rows, S, H, Hkv, D, ps, P, max_pages, batch.max_new, batch.max_total,
              qkv.data_ptr(), batch.cu_tokens.data_ptr(), batch.ctx_len.data_ptr(), batch.block_table.data_ptr(),
@@ -1054,10 +1063,10 @@ def paged_attention(q, batch: PagedBatch, cache: PagedCache, window: int = MQA_W
     if H < 1:
         raise ValueError("q must be [rows, H * D]")
     rows = q.shape[0]
-    _check(q, "q", (rows, H * D), torch.bfloat16, dev)
+    _need(q, "q", (rows, H * D), torch.bfloat16, dev)
     if out is None:
         out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
-    _check(out, "out", (rows, H * D), torch.bfloat16, dev)
+    _need(out, "out", (rows, H * D), torch.bfloat16, dev)
     if workspace is None:
         workspace = new_workspace(paged_attention_workspace_size(H, Hkv, D), dev)
     workspace, nb = _paged_workspace(workspace, 0, dev)
