@@ -17,6 +17,7 @@ namespace rglru {
 namespace {
 
 constexpr int kMaxN = 16384;
+constexpr int kSms = 148;
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
@@ -27,93 +28,125 @@ __device__ __forceinline__ uint32_t bf_pack(float lo, float hi)
     return r;
 }
 
-// One CTA per row, VPT vectors of 8 channels a thread; group == 0: bf16 output.
-template <int VPT, bool kE4m3>
+// A CTA walks over rows, VPT vectors of 8 channels a thread: the weight stays in registers, and the next row's loads
+// are issued before this row's sum is known.  group == 0: bf16 output.
+template <int VPT, bool kE4m3, bool kRes>
 __global__ void __launch_bounds__(512)
-rglru_add_rmsnorm_kernel(int N, int group, const uint4 *__restrict__ x, const uint4 *__restrict__ res,
-                         const float4 *__restrict__ w, float eps, uint4 *__restrict__ res_out, void *__restrict__ out,
+rglru_add_rmsnorm_kernel(int M, int N, int group, const uint4 *__restrict__ x, const uint4 *res,
+                         const float4 *__restrict__ w, float eps, uint4 *res_out, void *__restrict__ out,
                          float *__restrict__ out_scale)
 {
-    __shared__ float part[16];
+    __shared__ float part[2][16];
     const int tid = threadIdx.x, nvec = N / 8;
-    const size_t row = blockIdx.x;
-    uint4 v[VPT];
-    float ss = 0.f;
+    float4 wv[VPT][2];
+    uint4 v[VPT], r[VPT];
+    auto load = [&](int row) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int i = k * blockDim.x + tid;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (kRes) r[k] = make_uint4(0, 0, 0, 0);
+            if (i < nvec) {
+                v[k] = __ldcs(x + (size_t)row * nvec + i);
+                if (kRes) r[k] = __ldcs(res + (size_t)row * nvec + i);
+            }
+        }
+    };
+    load(blockIdx.x);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int i = k * blockDim.x + tid;
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (i < nvec) {
-            v[k] = x[row * nvec + i];
-            if (res != nullptr) {
-                const uint4 r = res[row * nvec + i];
-                v[k].x = bf_pack(bf_lo(v[k].x) + bf_lo(r.x), bf_hi(v[k].x) + bf_hi(r.x));
-                v[k].y = bf_pack(bf_lo(v[k].y) + bf_lo(r.y), bf_hi(v[k].y) + bf_hi(r.y));
-                v[k].z = bf_pack(bf_lo(v[k].z) + bf_lo(r.z), bf_hi(v[k].z) + bf_hi(r.z));
-                v[k].w = bf_pack(bf_lo(v[k].w) + bf_lo(r.w), bf_hi(v[k].w) + bf_hi(r.w));
-                res_out[row * nvec + i] = v[k];
+        wv[k][0] = i < nvec ? w[2 * i] : make_float4(0, 0, 0, 0);
+        wv[k][1] = i < nvec ? w[2 * i + 1] : make_float4(0, 0, 0, 0);
+    }
+    int turn = 0;
+    for (int row = blockIdx.x; row < M; row += gridDim.x, turn ^= 1) {
+        uint4 h[VPT];
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int i = k * blockDim.x + tid;
+            h[k] = v[k];
+            if (kRes) {
+                h[k].x = bf_pack(bf_lo(v[k].x) + bf_lo(r[k].x), bf_hi(v[k].x) + bf_hi(r[k].x));
+                h[k].y = bf_pack(bf_lo(v[k].y) + bf_lo(r[k].y), bf_hi(v[k].y) + bf_hi(r[k].y));
+                h[k].z = bf_pack(bf_lo(v[k].z) + bf_lo(r[k].z), bf_hi(v[k].z) + bf_hi(r[k].z));
+                h[k].w = bf_pack(bf_lo(v[k].w) + bf_lo(r[k].w), bf_hi(v[k].w) + bf_hi(r[k].w));
+                if (i < nvec) res_out[(size_t)row * nvec + i] = h[k];
+            }
+            const uint32_t q[4] = {h[k].x, h[k].y, h[k].z, h[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ss = fmaf(bf_lo(q[e]), bf_lo(q[e]), ss);
+                ss = fmaf(bf_hi(q[e]), bf_hi(q[e]), ss);
             }
         }
-        const uint32_t q[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        if (row + (int)gridDim.x < M) load(row + gridDim.x);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            ss = fmaf(bf_lo(q[e]), bf_lo(q[e]), ss);
-            ss = fmaf(bf_hi(q[e]), bf_hi(q[e]), ss);
-        }
-    }
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if ((tid & 31) == 0) part[turn][tid >> 5] = ss;  // two turns: a row's sums are read while the next row's are written
+        __syncthreads();
+        ss = 0.f;
+        for (int k = 0; k < (int)blockDim.x / 32; ++k) ss += part[turn][k];
+        const float inv = rsqrtf(ss / (float)N + eps);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if ((tid & 31) == 0) part[tid >> 5] = ss;
-    __syncthreads();
-    ss = 0.f;
-    for (int k = 0; k < (int)blockDim.x / 32; ++k) ss += part[k];
-    const float inv = rsqrtf(ss / (float)N + eps);
+        for (int k = 0; k < VPT; ++k) {
+            const int i = k * blockDim.x + tid;
+            const bool in = i < nvec;
+            const float4 wa = wv[k][0], wb = wv[k][1];
+            const float y[8] = {bf_lo(h[k].x) * inv * wa.x, bf_hi(h[k].x) * inv * wa.y, bf_lo(h[k].y) * inv * wa.z,
+                                bf_hi(h[k].y) * inv * wa.w, bf_lo(h[k].z) * inv * wb.x, bf_hi(h[k].z) * inv * wb.y,
+                                bf_lo(h[k].w) * inv * wb.z, bf_hi(h[k].w) * inv * wb.w};
+            if (!kE4m3) {
+                if (in)
+                    static_cast<uint4 *>(out)[(size_t)row * nvec + i] =
+                        make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));
+            } else {
+                // a group is group / 8 (4 to 32, a power of two) adjacent lanes of one warp
+                float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int i = k * blockDim.x + tid;
-        const bool in = i < nvec;
-        const float4 wa = in ? w[2 * i] : make_float4(0, 0, 0, 0), wb = in ? w[2 * i + 1] : make_float4(0, 0, 0, 0);
-        const float y[8] = {bf_lo(v[k].x) * inv * wa.x, bf_hi(v[k].x) * inv * wa.y, bf_lo(v[k].y) * inv * wa.z,
-                            bf_hi(v[k].y) * inv * wa.w, bf_lo(v[k].z) * inv * wb.x, bf_hi(v[k].z) * inv * wb.y,
-                            bf_lo(v[k].w) * inv * wb.z, bf_hi(v[k].w) * inv * wb.w};
-        if (!kE4m3) {
-            if (in)
-                static_cast<uint4 *>(out)[row * nvec + i] =
-                    make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));
-        } else {
-            // a group is group / 8 (4 to 32, a power of two) adjacent lanes of one warp
-            float amax = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
-            for (int o = group / 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float s = e4m3::scale_of(amax), r = e4m3::inverse(s);
-            if (in) {
-                static_cast<uint2 *>(out)[row * nvec + i] =
-                    make_uint2(e4m3::pack4(y[0] * r, y[1] * r, y[2] * r, y[3] * r),
-                               e4m3::pack4(y[4] * r, y[5] * r, y[6] * r, y[7] * r));
-                if (i % (group / 8) == 0) out_scale[row * (N / group) + i / (group / 8)] = s;
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
+                for (int o = group / 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                const float s = e4m3::scale_of(amax), f = e4m3::inverse(s);
+                if (in) {
+                    static_cast<uint2 *>(out)[(size_t)row * nvec + i] =
+                        make_uint2(e4m3::pack4(y[0] * f, y[1] * f, y[2] * f, y[3] * f),
+                                   e4m3::pack4(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
+                    if (i % (group / 8) == 0) out_scale[(size_t)row * (N / group) + i / (group / 8)] = s;
+                }
             }
         }
     }
+}
+
+template <int VPT, bool kE4m3>
+rglru_status launch_vpt(int M, int N, int group, const void *x, const void *res, const float *w, float eps, void *res_out,
+                        void *out, float *out_scale, cudaStream_t stream)
+{
+    const int threads = ((N / 8 + VPT - 1) / VPT + 31) / 32 * 32;
+    // resident threads: 2048 an SM fill it, but the bf16 form with one vector a thread runs better with 1536 (below)
+    const int most = kSms * ((VPT == 1 ? 1536 : 2048) / threads);
+    const int grid = M < most ? M : most;
+    const auto *xv = static_cast<const uint4 *>(x), *rv = static_cast<const uint4 *>(res);
+    const auto *wv = reinterpret_cast<const float4 *>(w);
+    auto *ro = static_cast<uint4 *>(res_out);
+    if (res != nullptr)
+        rglru_add_rmsnorm_kernel<VPT, kE4m3, true><<<grid, threads, 0, stream>>>(M, N, group, xv, rv, wv, eps, ro, out, out_scale);
+    else
+        rglru_add_rmsnorm_kernel<VPT, kE4m3, false><<<grid, threads, 0, stream>>>(M, N, group, xv, rv, wv, eps, ro, out, out_scale);
+    return cuda_status(cudaGetLastError());
 }
 
 template <bool kE4m3>
 rglru_status launch(int M, int N, int group, const void *x, const void *res, const float *w, float eps, void *res_out,
                     void *out, float *out_scale, cudaStream_t stream)
 {
-    const int nvec = N / 8;
-    const auto *xv = static_cast<const uint4 *>(x), *rv = static_cast<const uint4 *>(res);
-    const auto *wv = reinterpret_cast<const float4 *>(w);
-    auto *ro = static_cast<uint4 *>(res_out);
-    const int vpt = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-    const int threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
-    if (vpt == 1)
-        rglru_add_rmsnorm_kernel<1, kE4m3><<<M, threads, 0, stream>>>(N, group, xv, rv, wv, eps, ro, out, out_scale);
-    else if (vpt == 2)
-        rglru_add_rmsnorm_kernel<2, kE4m3><<<M, threads, 0, stream>>>(N, group, xv, rv, wv, eps, ro, out, out_scale);
-    else
-        rglru_add_rmsnorm_kernel<4, kE4m3><<<M, threads, 0, stream>>>(N, group, xv, rv, wv, eps, ro, out, out_scale);
-    return cuda_status(cudaGetLastError());
+    // 32768 x 2560, bf16: one vector a thread and 1536 threads an SM 106 us (97% of the measured bandwidth with the launch), 2048
+    // threads 117, two vectors 113.  The e4m3 form has the maxima's shuffles to hide: two vectors and 2048 threads 111 us, one
+    // vector 123 to 131; 4099 x 4096 27 us against 31.
+    if (!kE4m3 && N <= 4096) return launch_vpt<1, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
+    if (N <= 2 * 4096) return launch_vpt<2, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
+    return launch_vpt<4, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
 }
 
 rglru_status check(int M, int N, int group, const void *x, const void *res, const float *w, float eps,
