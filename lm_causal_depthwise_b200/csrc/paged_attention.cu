@@ -7,6 +7,8 @@
 #include "paged.cuh"
 #include "sm100.cuh"
 
+#include <climits>
+
 namespace rglru {
 namespace {
 
@@ -14,7 +16,7 @@ using paged::Batch;
 
 struct AttendArgs {
     Batch b;
-    int window;
+    int window, few;  // sequences of up to `few` rows (a head's) go to the 16-row kernel, the others to the 128-row one
     float scale;
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;
@@ -55,13 +57,15 @@ constexpr int kMeta = 8;  // k of tile t + kSlots - 1 takes the slot of v of til
 struct Plan {  // the unit that begins in a CTA's piece and does not end there: its parts, rows and first row's place
     int parts, rows, row0, row_head;  // row_head: first row (token * G + head in group) * 64 + key/value head
 };
-// Workspace: header, plans, then per CTA two partial results (slot 2 c: a unit begun in an earlier CTA; 2 c + 1: one begun
-// here) of 16 rows: m, mv, l, pad (float4) and O [16][D].
+// Workspace: header, plans, then partial results, R rows each: m, mv, l, pad (float4) and O [R][D].  The 16-row kernel has two a
+// CTA (slot 2 c: a unit begun in an earlier CTA; 2 c + 1: one begun here), the 128-row kernel one.
+constexpr int kWideRows = 128;
 constexpr size_t kPlanBytes = (size_t)kMaxCtas * sizeof(Plan);
-__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)kRowTile * (4 + D); }
+__host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size_t)rows * (4 + D); }
 inline size_t attention_bytes(int D)
 {
-    return kWsHeaderBytes + align_up_d(kPlanBytes, 256) + (size_t)kMaxCtas * 2 * part_floats(D) * 4;
+    const size_t few = (size_t)(D == 256 ? 2 : 3) * kSms * 2 * part_floats(kRowTile, D), wide = kSms * part_floats(kWideRows, D);
+    return kWsHeaderBytes + align_up_d(kPlanBytes, 256) + (few > wide ? few : wide) * 4;
 }
 
 struct Geometry {
@@ -71,7 +75,7 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs &p, int i)
 {
     const paged::Seq s = paged::load_seq(p.b, i);
     Geometry g = {s.row0, s.n, s.ctx, 0, 0, 0};
-    if (s.n > 0) {
+    if (s.n > 0 && (long long)s.n * (p.b.H / p.b.Hkv) <= p.few) {
         g.tile0 = max(0, s.ctx - p.window + 1) / kKeyTile;
         g.tiles = (s.ctx + s.n - 1) / kKeyTile - g.tile0 + 1;
         const int G = p.b.H / p.b.Hkv;
@@ -614,7 +618,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
             }
             consumer_sync();
             const bool whole = unit_first && last;
-            float *slot = parts + ((size_t)cta * 2 + (unit_first ? 1 : 0)) * part_floats(D);
+            float *slot = parts + ((size_t)cta * 2 + (unit_first ? 1 : 0)) * part_floats(kRowTile, D);
             if (!whole && unit_first)  // the unit began here and goes on: the later CTAs with a part of it
                 plan = {piece_of(total, end + mt.left - 1, n_ctas) - cta + 1, urows, row0, urow * 64 + head};
 #pragma unroll
@@ -660,7 +664,8 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
 // warps every eighth part.  Each CTA lists the items from the plans (one scan) and takes every gridDim.x-th.
 constexpr int kFewParts = 24, kJoinThreads = 1024;
 
-template <int D>
+// R: rows of a part
+template <int D, int R>
 __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const AttendArgs p, int n)
 {
     constexpr int kSlices = D / 64, kVec = D / 128, kWarps = kJoinThreads / 32;
@@ -716,7 +721,9 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
         }
         return lo;
     };
-    auto part = [&](int c, int k) { return parts + ((size_t)(c + k) * 2 + (k == 0)) * part_floats(D); };
+    auto part = [&](int c, int k) {
+        return parts + (R == kRowTile ? (size_t)(c + k) * 2 + (k == 0) : (size_t)(c + k)) * part_floats(R, D);
+    };
     auto out_row = [&](const Plan &pl, int r) {
         const int row = (pl.row_head >> 6) + r, head = pl.row_head & 63;
         return p.out + ((size_t)(pl.row0 + row / G) * b.H + head * G + row % G) * D;
@@ -732,7 +739,7 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int x = 0; x < kVec; ++x)
-                v0[k][x] = (reinterpret_cast<const float4 *>(part(c, k) + 4 * kRowTile + r * D) + lane)[32 * x];
+                v0[k][x] = (reinterpret_cast<const float4 *>(part(c, k) + 4 * R + r * D) + lane)[32 * x];
         float m = st.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -755,7 +762,7 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
 #pragma unroll 4
         for (int k = 2; k < pl.parts; ++k) {
             const float fk = __shfl_sync(0xffffffffu, f, k);
-            const float4 *src = reinterpret_cast<const float4 *>(part(c, k) + 4 * kRowTile + r * D) + lane;
+            const float4 *src = reinterpret_cast<const float4 *>(part(c, k) + 4 * R + r * D) + lane;
 #pragma unroll
             for (int x = 0; x < kVec; ++x) {
                 const float4 v = src[32 * x];
@@ -780,7 +787,7 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
             const int k = 2 * kWarps * x + 2 * warp + (lane >> 4);
             const bool in = k < pl.parts;
             st[x] = in ? *reinterpret_cast<const float4 *>(part(c, k) + 4 * r) : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-            v[x] = in ? *reinterpret_cast<const float4 *>(part(c, k) + 4 * kRowTile + r * D + ch + 4 * (lane & 15))
+            v[x] = in ? *reinterpret_cast<const float4 *>(part(c, k) + 4 * R + r * D + ch + 4 * (lane & 15))
                       : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         // m over the parts, then mv relative to it
@@ -842,26 +849,520 @@ bool encode_pool(CUtensorMap *m, const uint8_t *base, const Batch &b)
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ------------------------------------------------------------------------------------------------ 128 rows at a time
+// Chunks of tokens: products on tcgen05 with M = 128 rows (row = token * G + head in the group), 64 keys a tile.
+//   warps 0-3   softmax, thread = row = TMEM lane; warp 4 fetches pages by TMA as above; warps 5 and 6 issue S = Q K^T (Q
+//   from TMEM) and O += P V (P from TMEM); warps 7-10 turn the codes into f16: k into the K-major 128-byte swizzle, v
+//   into core matrices of 8 keys x 8 channels (its channels stay contiguous, so nothing is transposed).
+// One conversion serves 128 rows, so it hides under the products (128 x 64 x D twice: about 1000 cycles a tile at D = 256).
+// Exponents, scales and their references as in the 16-row kernel, with the references raised only when a row's
+// maximum passes them by 2^8 (P up to 2^8 keeps f16's bits), since moving O means a pass through TMEM.
+// A CTA takes whole units, and the last ones (fewer than CTAs) are cut into equal ranges of tiles: at most one part a
+// CTA, joined as above.
+constexpr int kWideThreads = 352;
+constexpr float kRaise = 8.f;
+
 template <int D>
-rglru_status launch(const AttendArgs &p, cudaStream_t stream)
+struct WideCfg {
+    static constexpr int kRaw = kKeyTile * D, kF16 = 2 * kRaw, kRawHalf = kKeyTile * 128, kBox = kKeyTile * 128;
+    static constexpr int kOffRawK = 0, kOffRawV = 2 * kRaw, kOffK = 4 * kRaw, kOffV = kOffK + 2 * kF16;
+    static constexpr int kSmem = kOffV + 2 * kF16 + 1024;
+    static constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384, kColP = 448;
+};
+
+struct Segment {  // a unit, or a range of its tiles
+    int head, row0, ctx, row, rows, pos0, pos1, lo, hi, seq;
+    int tile0, tiles;          // the range: first tile (of the positions), tiles
+    int parts, part;           // 1, 0: the whole unit
+};
+
+// Wide units of a sequence.
+__device__ __forceinline__ int wide_units(const AttendArgs &p, const paged::Seq &s)
 {
-    using C = Cfg<D>;
-    static PerDeviceFlag flag;
-    const rglru_status st =
-        set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_kernel<D>), C::kSmem, flag);
-    if (st != RGLRU_OK) return st;
-    CUtensorMap tm_k, tm_v;
-    if (!encode_pool(&tm_k, p.k, p.b) || !encode_pool(&tm_v, p.v, p.b)) return RGLRU_ERR_CUDA;
-    const int grid = kSms * C::kCtasPerSm;
-    rglru_paged_attention_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p, tm_k, tm_v);
-    if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
+    const long long rows = (long long)s.n * (p.b.H / p.b.Hkv);
+    return rows > p.few ? p.b.Hkv * (int)((rows + kWideRows - 1) / kWideRows) : 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 1)
+rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap tm_k,
+                                  const __grid_constant__ CUtensorMap tm_v)
+{
+    using namespace sm100;
+    using C = WideCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ Meta meta[kMeta];
+    __shared__ uint64_t rk_full[2], rk_free[2], rv_full[2], rv_free[2], k_full[2], k_free[2], v_full[2], v_free[2];
+    __shared__ uint64_t q_full, s_full, s_free, p_full[2], pv_done[2], drain[2];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int scan[kWideThreads / 32], nan_count, nan_key0[64];
+    __shared__ Segment seg_s;
+    const Batch &b = p.b;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = b.H / b.Hkv, cta = blockIdx.x, n_ctas = gridDim.x;
+    Plan *plans = reinterpret_cast<Plan *>(reinterpret_cast<char *>(b.ws) + kWsHeaderBytes);
+    float *parts = reinterpret_cast<float *>(reinterpret_cast<char *>(b.ws) + kWsHeaderBytes + align_up_d(kPlanBytes, 256));
+    griddep_launch_dependents();
+
+    if (warp == 5) {
+        tmem_alloc(&tmem_holder, 512);
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(rk_full + i, 1), mbar_init(rv_full + i, 1), mbar_init(rk_free + i, 4), mbar_init(rv_free + i, 4);
+                mbar_init(k_full + i, 4), mbar_init(v_full + i, 4), mbar_init(k_free + i, 1), mbar_init(v_free + i, 1);
+                mbar_init(p_full + i, 128), mbar_init(pv_done + i, 1), mbar_init(drain + i, 1);
+            }
+            mbar_init(&q_full, 128), mbar_init(&s_full, 1), mbar_init(&s_free, 128);
+            mbar_fence_init();
+        }
+    }
+    // this thread's sequences and the units before them
+    const int per = (b.S + kWideThreads - 1) / kWideThreads, s0 = min(b.S, tid * per), s1 = min(b.S, s0 + per);
+    int mine = 0;
+    for (int i = s0; i < s1; ++i) mine += wide_units(p, paged::load_seq(b, i));
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) scan[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int units = 0, before = inc - mine;
+    for (int w = 0; w < kWideThreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        units += scan[w];
+    }
+    const uint32_t tmem = tmem_holder;
+    const int whole = units / n_ctas * n_ctas, rest = units - whole, cuts = rest > 0 ? n_ctas / rest : 1;
+    if (tid == 0) plans[cta] = {0, 0, 0, 0};
+
+    int n = 0;          // tiles done before this segment: the phase of every barrier
+    bool alive = true;
+    for (int round = 0; round <= units / n_ctas; ++round) {
+        int unit = round * n_ctas + cta, part = 0;
+        if (round == units / n_ctas) {  // what is left, cut
+            if (cta / cuts >= rest) break;
+            unit = whole + cta / cuts, part = cta % cuts;
+        }
+        __syncthreads();  // the last segment is done with
+        if (unit >= before && unit < before + mine) {
+            int at = before;
+            for (int i = s0; i < s1; ++i) {
+                const paged::Seq s = paged::load_seq(b, i);
+                const int u = wide_units(p, s);
+                if (unit < at + u) {
+                    const int per_head = u / b.Hkv;
+                    Segment g;
+                    g.seq = i, g.row0 = s.row0, g.ctx = s.ctx;
+                    g.head = (unit - at) / per_head;
+                    g.row = (unit - at) % per_head * kWideRows;
+                    g.rows = (int)min((long long)kWideRows, (long long)s.n * G - g.row);
+                    g.pos0 = s.ctx + g.row / G, g.pos1 = s.ctx + (g.row + g.rows - 1) / G;
+                    g.lo = max(0, g.pos0 - p.window + 1), g.hi = g.pos1 + 1;
+                    g.tile0 = g.lo / kKeyTile;
+                    const int tiles = (g.hi - 1) / kKeyTile - g.tile0 + 1;
+                    g.parts = round < units / n_ctas ? 1 : max(1, min(cuts, tiles / kMinTiles));
+                    g.part = part;
+                    g.tiles = 0;
+                    if (part < g.parts) {
+                        const int from = (int)((long long)tiles * part / g.parts);
+                        g.tiles = (int)((long long)tiles * (part + 1) / g.parts) - from;
+                        g.tile0 += from;
+                    }
+                    seg_s = g;
+                    break;
+                }
+                at += u;
+            }
+        }
+        if (tid == 0) nan_count = 0;
+        __syncthreads();
+        const Segment seg = seg_s;
+        if (seg.tiles == 0) continue;
+        const int tiles = seg.tiles;
+
+        if (warp == 4) {
+            // ------------------------------------------------------------ pages by TMA
+            const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile);
+            for (int t0 = 0; t0 < tiles; t0 += 8) {
+                const int q = lane & 3, key0 = (seg.tile0 + t0 + (lane >> 2)) * kKeyTile, key = key0 + 16 * q;
+                int page = -1;
+                float ks = 0.f, vs = 0.f;
+                const int bk = key & ~(box - 1);  // the box's first key
+                if (t0 + (lane >> 2) < tiles && bk + box > seg.lo && bk < seg.hi) {
+                    page = b.table[(size_t)seg.seq * b.max_pages + (key >> page_shift)];
+                    if (page < 0 || page >= b.num_pages) {
+                        paged::record_invalid(b.ws);
+                        page = -1;
+                    }
+                }
+                const size_t at = (size_t)max(page, 0) * b.Hkv + seg.head;
+                if (page >= 0) ks = p.ks[at], vs = p.vs[at];
+                const bool ok = page >= 0 && key + 16 > seg.lo && key < seg.hi, leads = page >= 0 && key == bk;
+                const uint32_t oks = __ballot_sync(0xffffffffu, ok), leaders = __ballot_sync(0xffffffffu, leads);
+                const int c1 = (int)((at << page_shift) + (key & (b.page - 1)));
+                for (int t = 0; t < min(8, tiles - t0); ++t) {
+                    const int i = n + t0 + t, slot = i & 1;
+                    const uint32_t parity = (uint32_t)(i / 2 - 1) & 1u, bytes = (uint32_t)__popc(leaders & (0xfu << (4 * t))) * box * D;
+                    const bool lead = leads && (lane >> 2) == t;
+                    if (i >= 2 && alive) alive = wait(rk_free + slot, parity, b.ws, 10);
+                    if (lane == 0) mbar_expect(rk_full + slot, bytes);
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < D / 128; ++x)
+                        if (lead) tma_load_2d(smem + C::kOffRawK + slot * C::kRaw + x * C::kRawHalf + q * 2048, &tm_k, rk_full + slot, x * 128, c1);
+                    if ((lane >> 2) == t) {
+                        Meta &mt = meta[i % kMeta];
+                        mt.ks[q] = ks;
+                        mt.lv[q] = ok ? log2f(vs) : 0.f;
+                        if (q == 0) mt.ok = (int)((oks >> (4 * t)) & 0xfu), mt.key0 = key0;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rk_full + slot);
+                    if (i >= 2 && alive) alive = wait(rv_free + slot, parity, b.ws, 11);
+                    if (lane == 0) mbar_expect(rv_full + slot, bytes);
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < D / 128; ++x)
+                        if (lead) tma_load_2d(smem + C::kOffRawV + slot * C::kRaw + x * C::kRawHalf + q * 2048, &tm_v, rv_full + slot, x * 128, c1);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rv_full + slot);
+                }
+            }
+        } else if (warp >= 7) {
+            // ------------------------------------------------------------ codes to f16 operands
+            // a thread: one key, half of its 16-channel chunks; lanes are consecutive keys, so every phase of a
+            // read or write touches each bank once
+            const int cw = warp - 7, row = (cw & 1) * 32 + lane, c0 = (cw >> 1) * (D / 32);
+            for (int t = 0; t < tiles; ++t) {
+                const int i = n + t, slot = i & 1;
+                const uint32_t ph = (uint32_t)(i / 2) & 1u, freed = (uint32_t)(i / 2 - 1) & 1u;
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    if (alive) alive = wait((v ? rv_full : rk_full) + slot, ph, b.ws, 12 + v);
+                    if (i >= 2 && alive) alive = wait((v ? v_free : k_free) + slot, freed, b.ws, 14 + v);
+                    const Meta &mt = meta[i % kMeta];
+                    const int key0 = mt.key0, key = key0 + row;
+                    const bool in = ((mt.ok >> (row >> 4)) & 1) && key >= seg.lo && key < seg.hi;
+                    // rows that see different keys: a NaN of v must not reach those that do not see it
+                    const bool mixed = key0 < seg.pos1 - p.window + 1 || key0 + kKeyTile - 1 > seg.pos0;
+                    const uint8_t *src = smem + (v ? C::kOffRawV : C::kOffRawK) + slot * C::kRaw + row * 128;
+                    uint8_t *dst = smem + (v ? C::kOffV : C::kOffK) + slot * C::kF16;
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        const int c = c0 + x;
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (in) w = *reinterpret_cast<const uint4 *>(src + (c >> 3) * C::kRawHalf + (((c & 7) ^ (row & 7)) << 4));
+                        uint32_t u[4] = {w.x, w.y, w.z, w.w}, h[8];
+                        if (v && mixed) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t m = nan_bytes(u[e]);
+                                bad |= m;
+                                u[e] &= ~m;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) e4m3::to_f16x2x2(u[e], h[2 * e], h[2 * e + 1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int o = 2 * c + e;  // octet of channels
+                            uint8_t *to = v ? dst + o * 1024 + (row >> 3) * 128 + (row & 7) * 16
+                                            : dst + (o >> 3) * C::kBox + row * 128 + (((o & 7) ^ (row & 7)) << 4);
+                            *reinterpret_cast<uint4 *>(to) = make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, bad != 0) && lane == 0) {
+                        const int at = atomicAdd(&nan_count, 1);
+                        if (at < 64) nan_key0[at] = key0;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive((v ? v_full : k_full) + slot);
+                        mbar_arrive((v ? rv_free : rk_free) + slot);
+                    }
+                }
+            }
+        } else if (warp == 5) {
+            // ------------------------------------------------------------ S = Q K^T
+            const uint32_t idesc = umma_idesc_f16(kWideRows, kKeyTile);
+            for (int t = 0; t < tiles; ++t) {
+                const int i = n + t, slot = i & 1;
+                if (t == 0 && alive) alive = wait(&q_full, (uint32_t)round & 1u, b.ws, 16);
+                if (alive) alive = wait(k_full + slot, (uint32_t)(i / 2) & 1u, b.ws, 17);
+                if (i >= 1 && alive) alive = wait(&s_free, (uint32_t)(i - 1) & 1u, b.ws, 18);
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t kd = umma_desc_sw128(smem_u32(smem + C::kOffK + slot * C::kF16));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_ts_warp(tmem + C::kColS, tmem + C::kColQ + (uint32_t)kk * 8,
+                                 kd + (uint64_t)(((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4), idesc, kk > 0);
+                umma_commit_warp(&s_full);
+                umma_commit_warp(k_free + slot);
+                __syncwarp();
+            }
+        } else if (warp == 6) {
+            // ------------------------------------------------------------ O += P V
+            const uint32_t idesc = umma_idesc_f16(kWideRows, D) | (1u << 16);  // v's channels are contiguous
+            for (int t = 0; t < tiles; ++t) {
+                const int i = n + t, slot = i & 1;
+                if (alive) alive = wait(p_full + slot, (uint32_t)(i / 2) & 1u, b.ws, 19);
+                if (alive) alive = wait(v_full + slot, (uint32_t)(i / 2) & 1u, b.ws, 20);
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t vd = umma_desc_mn_noswizzle(smem_u32(smem + C::kOffV + slot * C::kF16), 128, 1024);
+#pragma unroll
+                for (int kk = 0; kk < kKeyTile / 16; ++kk)
+                    umma_ts_warp(tmem + C::kColO, tmem + C::kColP + (uint32_t)(slot * 32 + kk * 8), vd + (uint64_t)((kk * 256) >> 4),
+                                 idesc, (t > 0 || kk > 0) ? 1u : 0u);
+                umma_commit_warp(pv_done + slot);
+                umma_commit_warp(v_free + slot);
+                __syncwarp();
+            }
+        } else {
+            // ------------------------------------------------------------ softmax, thread = row
+            const int r = tid;
+            const bool live = r < seg.rows;
+            const int row = seg.row + (live ? r : 0), pos = seg.ctx + row / G;
+            const int lo = live ? max(0, pos - p.window + 1) : INT_MAX, hi = live ? pos : -1;
+            const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+            const size_t place = ((size_t)(seg.row0 + row / G) * b.H + seg.head * G + row % G) * D;
+            float qs;
+            {
+                // the row as f16, times a power of two that brings its largest exponent to 2^13; read twice, since 128 registers
+                // of it beside the scores spill
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + place);
+                uint32_t top = 0;
+#pragma unroll 16
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 q = live ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7f800000u, w[x] & 0x7f800000u));
+                }
+                int e = min(100, max(-100, (int)(top >> 23) - 127 - 13));
+                if (top == 0) e = 0;
+                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+                qs = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll 1
+                for (int g = 0; g < D / 64; ++g) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 q = live ? __ldg(src + 8 * g + k) : make_uint4(0, 0, 0, 0);
+                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) w[4 * k + x] = pack_f16(bf_lo(u[x]) * f, bf_hi(u[x]) * f);
+                    }
+                    __syncwarp();
+                    tmem_st32(tmem + lane_off + C::kColQ + (uint32_t)(g * 32), w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&q_full);
+            }
+            float m = -INFINITY, mv = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int t = 0; t < tiles; ++t) {
+                const int i = n + t, pb = i & 1;
+                if (alive) alive = wait(&s_full, (uint32_t)i & 1u, b.ws, 21);
+                __syncwarp();
+                tc_fence_after();
+                const Meta &mt = meta[i % kMeta];
+                const int key0 = mt.key0, okm = mt.ok;
+                float v[64];
+                {
+                    uint32_t ra[32], rb[32];
+                    tmem_ld32(tmem + lane_off + C::kColS, ra);
+                    tmem_ld32(tmem + lane_off + C::kColS + 32, rb);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    mbar_arrive(&s_free);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(ra[e]), v[e + 32] = __uint_as_float(rb[e]);
+                }
+                float lv[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float c = qs * mt.ks[g];
+                    lv[g] = mt.lv[g];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[16 * g + e] *= c;
+                }
+                const bool inside = okm == 15 && key0 >= lo && key0 + kKeyTile - 1 <= hi;
+                if (!__all_sync(0xffffffffu, inside)) {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (!((okm >> (e >> 4)) & 1) || key0 + e < lo || key0 + e > hi) v[e] = -INFINITY;
+                }
+                float gm[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    gm[g] = v[16 * g];
+#pragma unroll
+                    for (int e = 1; e < 16; ++e) gm[g] = fmaxf(gm[g], v[16 * g + e]);
+                }
+                const float mt_max = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
+                if (mt_max > m + kRaise || (m == -INFINITY && mt_max > m)) {  // a reference of its own for l; mv is relative to it
+                    if (m != -INFINITY) l *= ex2_approx(m - mt_max), mv += m - mt_max;
+                    m = mt_max;
+                }
+                const float mz = finite_or_0(m);
+                const float top = fmaxf(fmaxf(gm[0] - mz + lv[0], gm[1] - mz + lv[1]), fmaxf(gm[2] - mz + lv[2], gm[3] - mz + lv[3]));
+                float f = 1.f;
+                bool move = false;
+                if (top > mv + kRaise || (mv == -INFINITY && top > mv)) {
+                    move = mv != -INFINITY;
+                    if (move) f = ex2_approx(mv - top);
+                    mv = top;
+                }
+                if (__any_sync(0xffffffffu, move)) {
+                    // O holds the tiles before: wait for the last of them, then scale in place (a row moves after its first tile)
+                    if (alive) alive = wait(pv_done + ((i - 1) & 1), (uint32_t)((i - 1) / 2) & 1u, b.ws, 22);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(tmem + lane_off + C::kColO + (uint32_t)c, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                uint32_t pk[32];
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                const float vz = finite_or_0(mv);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    // below 2^126: a key whose 2^(s - m) underflows stays 0
+                    const float w = ex2_approx(fminf(lv[g] - vz, 126.f));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float p0 = ex2_approx(v[16 * g + 2 * e] - mz), p1 = ex2_approx(v[16 * g + 2 * e + 1] - mz);
+                        l4[e & 3] += p0 + p1;
+                        pk[8 * g + e] = pack_f16(p0 * w, p1 * w);
+                    }
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                // P's buffer was last read by the product of tile i - 2
+                if (i >= 2 && alive) alive = wait(pv_done + pb, (uint32_t)(i / 2 - 1) & 1u, b.ws, 23);
+                __syncwarp();
+                tc_fence_after();
+                tmem_st32(tmem + lane_off + C::kColP + (uint32_t)(pb * 32), pk);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + pb);
+            }
+            const int last = n + tiles - 1;
+            if (alive) alive = wait(pv_done + (last & 1), (uint32_t)(last / 2) & 1u, b.ws, 24);
+            __syncwarp();
+            tc_fence_after();
+            const int bad = min(nan_count, 64);
+            const bool is_whole = seg.parts == 1;
+            float *slot = parts + (size_t)cta * part_floats(kWideRows, D);
+            const float o_scale = l == 0.f ? 0.f : ex2_approx(finite_or_0(mv)) / l;
+            if (!is_whole && live && alive) *reinterpret_cast<float4 *>(slot + 4 * r) = make_float4(m, mv, l, 0.f);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)c, o);
+                tmem_wait_ld();
+                if (live && alive) {
+                for (int k = 0; k < bad; ++k)  // channels of NaN values that this row sees (listed tiles only, a few)
+                    for (int e = max(nan_key0[k], lo); e <= min(nan_key0[k] + kKeyTile - 1, hi); ++e) {
+                        const int page = b.table[(size_t)seg.seq * b.max_pages + e / b.page];
+                        if (page < 0 || page >= b.num_pages) continue;
+                        const uint8_t *src = p.v + (((size_t)page * b.Hkv + seg.head) * b.page + e % b.page) * D + c;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if ((src[x] & 0x7f) == 0x7f) o[x] = 0x7fc00000u;
+                    }
+                if (is_whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + place + c);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16(__uint_as_float(o[8 * x + 2 * e]) * o_scale, __uint_as_float(o[8 * x + 2 * e + 1]) * o_scale);
+                        dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(slot + 4 * kWideRows + (size_t)r * D + c);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                }
+                }
+                __syncwarp();
+            }
+            if (tid == 0 && !is_whole && seg.part == 0) plans[cta] = {seg.parts, seg.rows, seg.row0, seg.row * 64 + seg.head};
+            tc_fence_before();
+        }
+        n += tiles;
+    }
+    // no copy, product or read of TMEM is in flight when the CTA ends
+    __syncwarp();
+    if (warp == 5 || warp == 6) {
+        umma_commit_warp(drain + (warp - 5));
+        wait(drain + (warp - 5), 0, b.ws, 25);
+    }
+    if (warp == 4)
+        for (int i = max(0, n - 2); i < n; ++i) {
+            wait(rk_full + (i & 1), (uint32_t)(i / 2) & 1u, b.ws, 26);
+            wait(rv_full + (i & 1), (uint32_t)(i / 2) & 1u, b.ws, 27);
+        }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_dealloc(tmem, 512);
+}
+
+template <int D, int R>
+rglru_status launch_join(const AttendArgs &p, int grid, cudaStream_t stream)
+{
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kSms), cfg.blockDim = dim3(kJoinThreads), cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr, cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, rglru_paged_combine_kernel<D>, p, grid));
+    return cuda_status(cudaLaunchKernelEx(&cfg, rglru_paged_combine_kernel<D, R>, p, grid));
+}
+
+template <int D>
+rglru_status launch(AttendArgs p, cudaStream_t stream)
+{
+    using C = Cfg<D>;
+    using W = WideCfg<D>;
+    static PerDeviceFlag flag, wide_flag;
+    rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_kernel<D>), C::kSmem, flag);
+    if (st != RGLRU_OK) return st;
+    CUtensorMap tm_k, tm_v;
+    if (!encode_pool(&tm_k, p.k, p.b) || !encode_pool(&tm_v, p.v, p.b)) return RGLRU_ERR_CUDA;
+    // Sequences with more than two 16-row units go to the 128-row kernel: a unit's tile takes about as long there for all
+    // 128 rows as here for 16.  The 16-row kernel runs in any case: a batch may hold short runs beside long ones.
+    const bool wide = (int64_t)p.b.max_new * (p.b.H / p.b.Hkv) > 2 * kRowTile;
+    p.few = wide ? 2 * kRowTile : INT32_MAX;
+    const int grid = kSms * C::kCtasPerSm;
+    rglru_paged_attention_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p, tm_k, tm_v);
+    if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
+    st = launch_join<D, kRowTile>(p, grid, stream);
+    if (st != RGLRU_OK || !wide) return st;
+    st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_wide_kernel<D>), W::kSmem, wide_flag);
+    if (st != RGLRU_OK) return st;
+    rglru_paged_attention_wide_kernel<D><<<kSms, kWideThreads, W::kSmem, stream>>>(p, tm_k, tm_v);
+    if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
+    return launch_join<D, kWideRows>(p, kSms, stream);
 }
 
 }  // namespace
@@ -886,7 +1387,7 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
 {
     const AttendArgs p = {{rows, S, H, Hkv, head_dim, page_size, num_pages, max_pages, max_new, max_total, cu_tokens,
                            ctx_len, block_table, static_cast<WsHeader *>(workspace)},
-                          window, scale, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
+                          window, 0, scale, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
                           static_cast<const uint8_t *>(v_cache), k_scale, v_scale, static_cast<__nv_bfloat16 *>(out)};
     const size_t need = rglru_paged_attention_workspace_size(H, Hkv, head_dim);
     const rglru_status c = paged::check_batch(p.b, k_cache, k_scale, v_cache, v_scale, workspace_bytes, need);

@@ -209,7 +209,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// Same, with B N-major (its N index contiguous in memory).
+// The same with A and B f16.
+__host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// umma_idesc_bf16 with B N-major (its N index contiguous in memory).
 __host__ __device__ constexpr uint32_t umma_idesc_bf16_bn(int M, int N) { return umma_idesc_bf16(M, N) | (1u << 16); }
 // Shared-memory matrix descriptor of an MN-major operand without swizzle: core
 // matrices of 8 K rows x 16 bytes (8 MN elements); lbo = byte distance of the
