@@ -52,6 +52,18 @@ __device__ __forceinline__ void to_f16x2x2(uint32_t codes, uint32_t &lo, uint32_
         : "=r"(lo), "=r"(hi)
         : "r"(codes));
 }
+// Two f16 values as two e4m3 terms each, x = hi + lo: hi the nearest code, lo that of the rest.  hi keeps 4 significant
+// bits, lo 4 more of a rest of at most half hi's step: a bf16 x (8 bits) is exact while |x| >= 2^-2; below
+// that the error is at most 2^-10 absolutely (half of lo's smallest step).
+__device__ __forceinline__ void split2(uint32_t x, uint32_t &hi, uint32_t &lo)
+{
+    asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 f, r;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tcvt.rn.f16x2.e4m3x2 f, h;\n\t"
+        "sub.rn.f16x2 r, %2, f;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, r;\n\t"
+        "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "r"(x));
+}
 __device__ __forceinline__ void to_f32x2(uint32_t codes, float &lo, float &hi)
 {
     const uint32_t h = to_f16x2(codes);

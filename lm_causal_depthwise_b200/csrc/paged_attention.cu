@@ -852,20 +852,25 @@ bool encode_pool(CUtensorMap *m, const uint8_t *base, const Batch &b)
 // ------------------------------------------------------------------------------------------------ 128 rows at a time
 // Chunks of tokens: products on tcgen05 with M = 128 rows (row = token * G + head in the group), 64 keys a tile.
 //   warps 0-3   softmax, thread = row = TMEM lane; warp 4 fetches pages by TMA as above; warps 5 and 6 issue S = Q K^T (Q
-//   from TMEM) and O += P V (P from TMEM); warps 7-10 turn the codes into f16: k into the K-major 128-byte swizzle, v
-//   into core matrices of 8 keys x 8 channels (its channels stay contiguous, so nothing is transposed).
-// One conversion serves 128 rows, so it hides under the products (128 x 64 x D twice: about 1000 cycles a tile at D = 256).
+//   from TMEM) and O += P V (P from TMEM); warps 7-14 turn v's codes into f16 core matrices of 8 keys x 8 channels (its
+//   channels stay contiguous, so nothing is transposed).
+// k's codes are operands as they arrive: the e4m3 product takes q as two e4m3 terms (e4m3.cuh: exact for all but values below
+// 2^-10 of the row's largest) at twice the f16 rate.  With k converted too, a tile moved 192 KB through shared memory
+// and took 2.0 us, its converters the longest wait; P stays f16, since two e4m3 terms of it would lose the keys
+// below 2^-18 of a row's largest, whose sum counts in a long cache.
 // Exponents, scales and their references as in the 16-row kernel, with the references raised only when a row's
 // maximum passes them by 2^8 (P up to 2^8 keeps f16's bits), since moving O means a pass through TMEM.
 // A CTA takes whole units, and the last ones (fewer than CTAs) are cut into equal ranges of tiles: at most one part a
 // CTA, joined as above.
-constexpr int kWideThreads = 352;
+constexpr int kWideThreads = 480;
 constexpr float kRaise = 8.f;
+constexpr int kNanTiles = 128;  // 8 warps' notes of the tiles that some rows of a unit see and others do not: at most 6 of them
 
 template <int D>
 struct WideCfg {
-    static constexpr int kRaw = kKeyTile * D, kF16 = 2 * kRaw, kRawHalf = kKeyTile * 128, kBox = kKeyTile * 128;
-    static constexpr int kOffRawK = 0, kOffRawV = 2 * kRaw, kOffK = 4 * kRaw, kOffV = kOffK + 2 * kF16;
+    static constexpr int kRing = 3;  // tiles of codes in flight
+    static constexpr int kRaw = kKeyTile * D, kF16 = 2 * kRaw, kRawHalf = kKeyTile * 128;
+    static constexpr int kOffRawK = 0, kOffRawV = kRing * kRaw, kOffV = 2 * kRing * kRaw;
     static constexpr int kSmem = kOffV + 2 * kF16 + 1024;
     static constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384, kColP = 448;
 };
@@ -893,10 +898,11 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Meta meta[kMeta];
-    __shared__ uint64_t rk_full[2], rk_free[2], rv_full[2], rv_free[2], k_full[2], k_free[2], v_full[2], v_free[2];
+    constexpr int kRing = C::kRing;
+    __shared__ uint64_t k_full[kRing], k_free[kRing], rv_full[kRing], rv_free[kRing], v_full[2], v_free[2];
     __shared__ uint64_t q_full, s_full, s_free, p_full[2], pv_done[2], drain[2];
     __shared__ uint32_t tmem_holder;
-    __shared__ int scan[kWideThreads / 32], nan_count, nan_key0[64];
+    __shared__ int scan[kWideThreads / 32], nan_count, nan_key0[kNanTiles];
     __shared__ Segment seg_s;
     const Batch &b = p.b;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = b.H / b.Hkv, cta = blockIdx.x, n_ctas = gridDim.x;
@@ -907,9 +913,10 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     if (warp == 5) {
         tmem_alloc(&tmem_holder, 512);
         if (lane == 0) {
+            for (int i = 0; i < kRing; ++i)
+                mbar_init(k_full + i, 1), mbar_init(k_free + i, 1), mbar_init(rv_full + i, 1), mbar_init(rv_free + i, 8);
             for (int i = 0; i < 2; ++i) {
-                mbar_init(rk_full + i, 1), mbar_init(rv_full + i, 1), mbar_init(rk_free + i, 4), mbar_init(rv_free + i, 4);
-                mbar_init(k_full + i, 4), mbar_init(v_full + i, 4), mbar_init(k_free + i, 1), mbar_init(v_free + i, 1);
+                mbar_init(v_full + i, 8), mbar_init(v_free + i, 1);
                 mbar_init(p_full + i, 128), mbar_init(pv_done + i, 1), mbar_init(drain + i, 1);
             }
             mbar_init(&q_full, 128), mbar_init(&s_full, 1), mbar_init(&s_free, 128);
@@ -1005,15 +1012,15 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 const uint32_t oks = __ballot_sync(0xffffffffu, ok), leaders = __ballot_sync(0xffffffffu, leads);
                 const int c1 = (int)((at << page_shift) + (key & (b.page - 1)));
                 for (int t = 0; t < min(8, tiles - t0); ++t) {
-                    const int i = n + t0 + t, slot = i & 1;
-                    const uint32_t parity = (uint32_t)(i / 2 - 1) & 1u, bytes = (uint32_t)__popc(leaders & (0xfu << (4 * t))) * box * D;
+                    const int i = n + t0 + t, slot = i % kRing;
+                    const uint32_t parity = (uint32_t)(i / kRing - 1) & 1u, bytes = (uint32_t)__popc(leaders & (0xfu << (4 * t))) * box * D;
                     const bool lead = leads && (lane >> 2) == t;
-                    if (i >= 2 && alive) alive = wait(rk_free + slot, parity, b.ws, 10);
-                    if (lane == 0) mbar_expect(rk_full + slot, bytes);
+                    if (i >= kRing && alive) alive = wait(k_free + slot, parity, b.ws, 10);
+                    if (lane == 0) mbar_expect(k_full + slot, bytes);
                     __syncwarp();
 #pragma unroll
                     for (int x = 0; x < D / 128; ++x)
-                        if (lead) tma_load_2d(smem + C::kOffRawK + slot * C::kRaw + x * C::kRawHalf + q * 2048, &tm_k, rk_full + slot, x * 128, c1);
+                        if (lead) tma_load_2d(smem + C::kOffRawK + slot * C::kRaw + x * C::kRawHalf + q * 2048, &tm_k, k_full + slot, x * 128, c1);
                     if ((lane >> 2) == t) {
                         Meta &mt = meta[i % kMeta];
                         mt.ks[q] = ks;
@@ -1021,8 +1028,8 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                         if (q == 0) mt.ok = (int)((oks >> (4 * t)) & 0xfu), mt.key0 = key0;
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(rk_full + slot);
-                    if (i >= 2 && alive) alive = wait(rv_free + slot, parity, b.ws, 11);
+                    if (lane == 0) mbar_arrive(k_full + slot);
+                    if (i >= kRing && alive) alive = wait(rv_free + slot, parity, b.ws, 11);
                     if (lane == 0) mbar_expect(rv_full + slot, bytes);
                     __syncwarp();
 #pragma unroll
@@ -1033,76 +1040,70 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 }
             }
         } else if (warp >= 7) {
-            // ------------------------------------------------------------ codes to f16 operands
-            // a thread: one key, half of its 16-channel chunks; lanes are consecutive keys, so every phase of a
+            // ------------------------------------------------------------ v's codes to f16 operands
+            // a thread: one key, a quarter of its 16-channel chunks; lanes are consecutive keys, so every phase of a
             // read or write touches each bank once
-            const int cw = warp - 7, row = (cw & 1) * 32 + lane, c0 = (cw >> 1) * (D / 32);
+            const int cw = warp - 7, row = (cw & 1) * 32 + lane, c0 = (cw >> 1) * (D / 64);
             for (int t = 0; t < tiles; ++t) {
-                const int i = n + t, slot = i & 1;
-                const uint32_t ph = (uint32_t)(i / 2) & 1u, freed = (uint32_t)(i / 2 - 1) & 1u;
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v) {
-                    if (alive) alive = wait((v ? rv_full : rk_full) + slot, ph, b.ws, 12 + v);
-                    if (i >= 2 && alive) alive = wait((v ? v_free : k_free) + slot, freed, b.ws, 14 + v);
-                    const Meta &mt = meta[i % kMeta];
-                    const int key0 = mt.key0, key = key0 + row;
-                    const bool in = ((mt.ok >> (row >> 4)) & 1) && key >= seg.lo && key < seg.hi;
-                    // rows that see different keys: a NaN of v must not reach those that do not see it
-                    const bool mixed = key0 < seg.pos1 - p.window + 1 || key0 + kKeyTile - 1 > seg.pos0;
-                    const uint8_t *src = smem + (v ? C::kOffRawV : C::kOffRawK) + slot * C::kRaw + row * 128;
-                    uint8_t *dst = smem + (v ? C::kOffV : C::kOffK) + slot * C::kF16;
-                    uint32_t bad = 0;
+                const int i = n + t, raw = i % kRing, slot = i & 1;
+                if (alive) alive = wait(rv_full + raw, (uint32_t)(i / kRing) & 1u, b.ws, 12);
+                if (i >= 2 && alive) alive = wait(v_free + slot, (uint32_t)(i / 2 - 1) & 1u, b.ws, 13);
+                const Meta &mt = meta[i % kMeta];
+                const int key0 = mt.key0, key = key0 + row;
+                const bool in = ((mt.ok >> (row >> 4)) & 1) && key >= seg.lo && key < seg.hi;
+                // rows that see different keys: a NaN must not reach those that do not see it
+                const bool mixed = key0 < seg.pos1 - p.window + 1 || key0 + kKeyTile - 1 > seg.pos0;
+                const uint8_t *src = smem + C::kOffRawV + raw * C::kRaw + row * 128;
+                uint8_t *dst = smem + C::kOffV + slot * C::kF16 + (row >> 3) * 128 + (row & 7) * 16;
+                uint32_t bad = 0;
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        const int c = c0 + x;
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (in) w = *reinterpret_cast<const uint4 *>(src + (c >> 3) * C::kRawHalf + (((c & 7) ^ (row & 7)) << 4));
-                        uint32_t u[4] = {w.x, w.y, w.z, w.w}, h[8];
-                        if (v && mixed) {
+                for (int x = 0; x < D / 64; ++x) {
+                    const int c = c0 + x;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (in) w = *reinterpret_cast<const uint4 *>(src + (c >> 3) * C::kRawHalf + (((c & 7) ^ (row & 7)) << 4));
+                    uint32_t u[4] = {w.x, w.y, w.z, w.w}, h[8];
+                    if (mixed) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t m = nan_bytes(u[e]);
-                                bad |= m;
-                                u[e] &= ~m;
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) e4m3::to_f16x2x2(u[e], h[2 * e], h[2 * e + 1]);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int o = 2 * c + e;  // octet of channels
-                            uint8_t *to = v ? dst + o * 1024 + (row >> 3) * 128 + (row & 7) * 16
-                                            : dst + (o >> 3) * C::kBox + row * 128 + (((o & 7) ^ (row & 7)) << 4);
-                            *reinterpret_cast<uint4 *>(to) = make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t m = nan_bytes(u[e]);
+                            bad |= m;
+                            u[e] &= ~m;
                         }
                     }
-                    if (__any_sync(0xffffffffu, bad != 0) && lane == 0) {
-                        const int at = atomicAdd(&nan_count, 1);
-                        if (at < 64) nan_key0[at] = key0;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive((v ? v_full : k_full) + slot);
-                        mbar_arrive((v ? rv_free : rk_free) + slot);
-                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) e4m3::to_f16x2x2(u[e], h[2 * e], h[2 * e + 1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)  // octets of channels
+                        *reinterpret_cast<uint4 *>(dst + (2 * c + e) * 1024) = make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                }
+                if (__any_sync(0xffffffffu, bad != 0) && lane == 0) {
+                    const int at = atomicAdd(&nan_count, 1);
+                    if (at < kNanTiles) nan_key0[at] = key0;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(v_full + slot);
+                    mbar_arrive(rv_free + raw);
                 }
             }
         } else if (warp == 5) {
             // ------------------------------------------------------------ S = Q K^T
-            const uint32_t idesc = umma_idesc_f16(kWideRows, kKeyTile);
+            const uint32_t idesc = umma_idesc_e4m3(kWideRows, kKeyTile);
             for (int t = 0; t < tiles; ++t) {
-                const int i = n + t, slot = i & 1;
+                const int i = n + t, slot = i % kRing;
                 if (t == 0 && alive) alive = wait(&q_full, (uint32_t)round & 1u, b.ws, 16);
-                if (alive) alive = wait(k_full + slot, (uint32_t)(i / 2) & 1u, b.ws, 17);
+                if (alive) alive = wait(k_full + slot, (uint32_t)(i / kRing) & 1u, b.ws, 17);
                 if (i >= 1 && alive) alive = wait(&s_free, (uint32_t)(i - 1) & 1u, b.ws, 18);
                 __syncwarp();
                 tc_fence_after();
-                const uint64_t kd = umma_desc_sw128(smem_u32(smem + C::kOffK + slot * C::kF16));
+                const uint64_t kd = umma_desc_sw128(smem_u32(smem + C::kOffRawK + slot * C::kRaw));
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_ts_warp(tmem + C::kColS, tmem + C::kColQ + (uint32_t)kk * 8,
-                                 kd + (uint64_t)(((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4), idesc, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) {  // the first terms, then the second
+                    const int c = kk % (D / 32);       // 32 channels: 32 bytes into 128-byte rows, 128 channels a half
+                    umma_ts_e4m3_warp(tmem + C::kColS, tmem + C::kColQ + (uint32_t)kk * 8,
+                                      kd + (uint64_t)(((c >> 2) * C::kRawHalf + (c & 3) * 32) >> 4), idesc, kk > 0);
+                }
                 umma_commit_warp(&s_full);
                 umma_commit_warp(k_free + slot);
                 __syncwarp();
@@ -1135,8 +1136,8 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             const size_t place = ((size_t)(seg.row0 + row / G) * b.H + seg.head * G + row % G) * D;
             float qs;
             {
-                // the row as f16, times a power of two that brings its largest exponent to 2^13; read twice, since 128 registers
-                // of it beside the scores spill
+                // the row as two e4m3 terms, times a power of two that brings its largest exponent to 2^7; read twice, since 128
+                // registers of it beside the scores spill
                 const uint4 *src = reinterpret_cast<const uint4 *>(p.q + place);
                 uint32_t top = 0;
 #pragma unroll 16
@@ -1146,22 +1147,35 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
 #pragma unroll
                     for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7f800000u, w[x] & 0x7f800000u));
                 }
-                int e = min(100, max(-100, (int)(top >> 23) - 127 - 13));
+                int e = min(100, max(-100, (int)(top >> 23) - 127 - 7));
                 if (top == 0) e = 0;
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
                 qs = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+                if (top == 0x7f800000u) qs = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row: codes saturate, so say it here
 #pragma unroll 1
-                for (int g = 0; g < D / 64; ++g) {
-                    uint32_t w[32];
+                for (int g = 0; g < D / 64; ++g) {  // 64 channels: 16 columns of each term
+                    uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint4 q = live ? __ldg(src + 8 * g + k) : make_uint4(0, 0, 0, 0);
                         const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) w[4 * k + x] = pack_f16(bf_lo(u[x]) * f, bf_hi(u[x]) * f);
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t h0, l0, h1, l1;
+                            e4m3::split2(pack_f16(bf_lo(u[2 * x]) * f, bf_hi(u[2 * x]) * f), h0, l0);
+                            e4m3::split2(pack_f16(bf_lo(u[2 * x + 1]) * f, bf_hi(u[2 * x + 1]) * f), h1, l1);
+                            hi[2 * k + x] = h0 | (h1 << 16), lo[2 * k + x] = l0 | (l1 << 16);
+                        }
                     }
                     __syncwarp();
-                    tmem_st32(tmem + lane_off + C::kColQ + (uint32_t)(g * 32), w);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t a[8], c[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) a[k] = hi[8 * x + k], c[k] = lo[8 * x + k];
+                        tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(g * 16 + x * 8), a);
+                        tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(D / 4 + g * 16 + x * 8), c);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1267,7 +1281,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             if (alive) alive = wait(pv_done + (last & 1), (uint32_t)(last / 2) & 1u, b.ws, 24);
             __syncwarp();
             tc_fence_after();
-            const int bad = min(nan_count, 64);
+            const int bad = min(nan_count, kNanTiles);
             const bool is_whole = seg.parts == 1;
             float *slot = parts + (size_t)cta * part_floats(kWideRows, D);
             const float o_scale = l == 0.f ? 0.f : ex2_approx(finite_or_0(mv)) / l;
@@ -1317,9 +1331,9 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
         wait(drain + (warp - 5), 0, b.ws, 25);
     }
     if (warp == 4)
-        for (int i = max(0, n - 2); i < n; ++i) {
-            wait(rk_full + (i & 1), (uint32_t)(i / 2) & 1u, b.ws, 26);
-            wait(rv_full + (i & 1), (uint32_t)(i / 2) & 1u, b.ws, 27);
+        for (int i = max(0, n - kRing); i < n; ++i) {
+            wait(k_full + i % kRing, (uint32_t)(i / kRing) & 1u, b.ws, 26);
+            wait(rv_full + i % kRing, (uint32_t)(i / kRing) & 1u, b.ws, 27);
         }
     tc_fence_before();
     __syncthreads();

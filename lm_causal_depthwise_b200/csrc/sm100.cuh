@@ -214,6 +214,8 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N)
 {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// kind::f8f6f4, A and B e4m3 (type code 0, as f16 has in kind::f16), D fp32.
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) { return umma_idesc_f16(M, N); }
 // umma_idesc_bf16 with B N-major (its N index contiguous in memory).
 __host__ __device__ constexpr uint32_t umma_idesc_bf16_bn(int M, int N) { return umma_idesc_bf16(M, N) | (1u << 16); }
 // Shared-memory matrix descriptor of an MN-major operand without swizzle: core
@@ -243,6 +245,16 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with both operands e4m3 (32 per step; four to a TMEM column), D fp32.
+__device__ __forceinline__ void umma_ts_e4m3_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
