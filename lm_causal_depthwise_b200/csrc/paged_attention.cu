@@ -16,7 +16,7 @@ using paged::Batch;
 
 struct AttendArgs {
     Batch b;
-    int window, few;  // sequences of up to `few` rows (a head's) go to the 16-row kernel, the others to the 128-row one
+    int window;
     float scale;
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;
@@ -75,7 +75,7 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs &p, int i)
 {
     const paged::Seq s = paged::load_seq(p.b, i);
     Geometry g = {s.row0, s.n, s.ctx, 0, 0, 0};
-    if (s.n > 0 && (long long)s.n * (p.b.H / p.b.Hkv) <= p.few) {
+    if (s.n > 0) {
         g.tile0 = max(0, s.ctx - p.window + 1) / kKeyTile;
         g.tiles = (s.ctx + s.n - 1) / kKeyTile - g.tile0 + 1;
         const int G = p.b.H / p.b.Hkv;
@@ -871,7 +871,9 @@ struct WideCfg {
     static constexpr int kRing = 3;  // tiles of codes in flight
     static constexpr int kRaw = kKeyTile * D, kF16 = 2 * kRaw, kRawHalf = kKeyTile * 128;
     static constexpr int kOffRawK = 0, kOffRawV = kRing * kRaw, kOffV = 2 * kRing * kRaw;
-    static constexpr int kSmem = kOffV + 2 * kF16 + 1024;
+    static constexpr int kOffStage = kOffV + 2 * kF16;     // per softmax warp: 32 rows x 32 channels of O on their way out
+    static constexpr int kSmem = kOffStage + 4 * 4096 + 1024;
+    static_assert(4 * 32 * 2 * D <= 2 * kF16, "the rows of q pass through v's operands' place");
     static constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384, kColP = 448;
 };
 
@@ -884,8 +886,7 @@ struct Segment {  // a unit, or a range of its tiles
 // Wide units of a sequence.
 __device__ __forceinline__ int wide_units(const AttendArgs &p, const paged::Seq &s)
 {
-    const long long rows = (long long)s.n * (p.b.H / p.b.Hkv);
-    return rows > p.few ? p.b.Hkv * (int)((rows + kWideRows - 1) / kWideRows) : 0;
+    return p.b.Hkv * (int)(((long long)s.n * (p.b.H / p.b.Hkv) + kWideRows - 1) / kWideRows);
 }
 
 template <int D>
@@ -1047,6 +1048,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             for (int t = 0; t < tiles; ++t) {
                 const int i = n + t, raw = i % kRing, slot = i & 1;
                 if (alive) alive = wait(rv_full + raw, (uint32_t)(i / kRing) & 1u, b.ws, 12);
+                if (t == 0 && alive) alive = wait(&q_full, (uint32_t)round & 1u, b.ws, 28);  // q has left this place
                 if (i >= 2 && alive) alive = wait(v_free + slot, (uint32_t)(i / 2 - 1) & 1u, b.ws, 13);
                 const Meta &mt = meta[i % kMeta];
                 const int key0 = mt.key0, key = key0 + row;
@@ -1131,19 +1133,43 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             const int r = tid;
             const bool live = r < seg.rows;
             const int row = seg.row + (live ? r : 0), pos = seg.ctx + row / G;
-            const int lo = live ? max(0, pos - p.window + 1) : INT_MAX, hi = live ? pos : -1;
+            // rows behind the unit's see everything: they are not written, and their tiles need no mask
+            const int lo = live ? max(0, pos - p.window + 1) : 0, hi = live ? pos : INT_MAX;
             const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-            const size_t place = ((size_t)(seg.row0 + row / G) * b.H + seg.head * G + row % G) * D;
+            uint8_t *stage = smem + C::kOffStage + warp * 4096, *rows_q = smem + C::kOffV + warp * 64 * D;
             float qs;
             {
-                // the row as two e4m3 terms, times a power of two that brings its largest exponent to 2^7; read twice, since 128
-                // registers of it beside the scores spill
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + place);
+                // The row as two e4m3 terms, times a power of two that brings its largest exponent to 2^7.  A warp fetches whole rows
+                // (a thread fetching its own touches 32 lines an instruction: 4 us), which meet their lane in shared memory, 16-byte
+                // piece x of row r at x ^ r: in the place of v's operands, whose converters wait for q.
+                constexpr int kPerRow = D / 8, kRowsAtOnce = 32 / kPerRow;  // 16-byte pieces of a row; rows of an instruction
+                const int sub = lane / kPerRow, piece = lane % kPerRow;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    uint4 q[16 / kRowsAtOnce];
+#pragma unroll
+                    for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
+                        const int at = part * 16 + k * kRowsAtOnce + sub, gr = seg.row + warp * 32 + at;
+                        q[k] = warp * 32 + at < seg.rows
+                                   ? __ldg(reinterpret_cast<const uint4 *>(
+                                         p.q + ((size_t)(seg.row0 + gr / G) * b.H + seg.head * G + gr % G) * D) + piece)
+                                   : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
+                        const int at = part * 16 + k * kRowsAtOnce + sub;
+                        *reinterpret_cast<uint4 *>(rows_q + at * 2 * D + ((piece ^ (at & (kPerRow - 1))) << 4)) = q[k];
+                    }
+                }
+                __syncwarp();
+                auto mine_q = [&](int k) {
+                    return *reinterpret_cast<const uint4 *>(rows_q + lane * 2 * D + ((k ^ (lane & (kPerRow - 1))) << 4));
+                };
                 uint32_t top = 0;
-#pragma unroll 16
+#pragma unroll 8
                 for (int k = 0; k < D / 8; ++k) {
-                    const uint4 q = live ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                    const uint4 u = mine_q(k);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7f800000u, w[x] & 0x7f800000u));
                 }
@@ -1151,31 +1177,24 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 if (top == 0) e = 0;
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
                 qs = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-                if (top == 0x7f800000u) qs = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row: codes saturate, so say it here
-#pragma unroll 1
-                for (int g = 0; g < D / 64; ++g) {  // 64 channels: 16 columns of each term
-                    uint32_t hi[16], lo[16];
+                if (top == 0x7f800000u) qs = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row: codes saturate
+#pragma unroll 2
+                for (int g = 0; g < D / 32; ++g) {  // 32 channels: 8 columns of each term
+                    uint32_t hi[8], lo_[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint4 q = live ? __ldg(src + 8 * g + k) : make_uint4(0, 0, 0, 0);
-                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 q4 = mine_q(4 * g + k);
+                        const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             uint32_t h0, l0, h1, l1;
                             e4m3::split2(pack_f16(bf_lo(u[2 * x]) * f, bf_hi(u[2 * x]) * f), h0, l0);
                             e4m3::split2(pack_f16(bf_lo(u[2 * x + 1]) * f, bf_hi(u[2 * x + 1]) * f), h1, l1);
-                            hi[2 * k + x] = h0 | (h1 << 16), lo[2 * k + x] = l0 | (l1 << 16);
+                            hi[2 * k + x] = h0 | (h1 << 16), lo_[2 * k + x] = l0 | (l1 << 16);
                         }
                     }
-                    __syncwarp();
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t a[8], c[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) a[k] = hi[8 * x + k], c[k] = lo[8 * x + k];
-                        tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(g * 16 + x * 8), a);
-                        tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(D / 4 + g * 16 + x * 8), c);
-                    }
+                    tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(g * 8), hi);
+                    tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(D / 4 + g * 8), lo_);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1190,7 +1209,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 tc_fence_after();
                 const Meta &mt = meta[i % kMeta];
                 const int key0 = mt.key0, okm = mt.ok;
-                float v[64];
+                f2_t v[32];  // pairs of scores
                 {
                     uint32_t ra[32], rb[32];
                     tmem_ld32(tmem + lane_off + C::kColS, ra);
@@ -1199,28 +1218,35 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     tc_fence_before();
                     mbar_arrive(&s_free);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(ra[e]), v[e + 32] = __uint_as_float(rb[e]);
+                    for (int e = 0; e < 16; ++e) {
+                        v[e] = f2_make(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1]));
+                        v[e + 16] = f2_make(__uint_as_float(rb[2 * e]), __uint_as_float(rb[2 * e + 1]));
+                    }
                 }
                 float lv[4];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const float c = qs * mt.ks[g];
+                    const f2_t c = f2_splat(qs * mt.ks[g]);
                     lv[g] = mt.lv[g];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[16 * g + e] *= c;
+                    for (int e = 0; e < 8; ++e) v[8 * g + e] = f2_mul(v[8 * g + e], c);
                 }
                 const bool inside = okm == 15 && key0 >= lo && key0 + kKeyTile - 1 <= hi;
                 if (!__all_sync(0xffffffffu, inside)) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (!((okm >> (e >> 4)) & 1) || key0 + e < lo || key0 + e > hi) v[e] = -INFINITY;
+                    for (int e = 0; e < 32; ++e) {
+                        const bool ok = (okm >> (e >> 3)) & 1;
+                        const int k = key0 + 2 * e;
+                        v[e] = f2_make(!ok || k < lo || k > hi ? -INFINITY : f2_lo(v[e]),
+                                       !ok || k + 1 < lo || k + 1 > hi ? -INFINITY : f2_hi(v[e]));
+                    }
                 }
                 float gm[4];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    gm[g] = v[16 * g];
+                    gm[g] = fmaxf(f2_lo(v[8 * g]), f2_hi(v[8 * g]));
 #pragma unroll
-                    for (int e = 1; e < 16; ++e) gm[g] = fmaxf(gm[g], v[16 * g + e]);
+                    for (int e = 1; e < 8; ++e) gm[g] = fmaxf(gm[g], fmaxf(f2_lo(v[8 * g + e]), f2_hi(v[8 * g + e])));
                 }
                 const float mt_max = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
                 if (mt_max > m + kRaise || (m == -INFINITY && mt_max > m)) {  // a reference of its own for l; mv is relative to it
@@ -1254,20 +1280,24 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     tc_fence_before();
                 }
                 uint32_t pk[32];
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                f2_t l2[2] = {f2_splat(0.f), f2_splat(0.f)};
                 const float vz = finite_or_0(mv);
+                const f2_t minus = f2_splat(-mz);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     // below 2^126: a key whose 2^(s - m) underflows stays 0
-                    const float w = ex2_approx(fminf(lv[g] - vz, 126.f));
+                    const f2_t w = f2_splat(ex2_approx(fminf(lv[g] - vz, 126.f)));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float p0 = ex2_approx(v[16 * g + 2 * e] - mz), p1 = ex2_approx(v[16 * g + 2 * e + 1] - mz);
-                        l4[e & 3] += p0 + p1;
-                        pk[8 * g + e] = pack_f16(p0 * w, p1 * w);
+                        const f2_t x = f2_add(v[8 * g + e], minus);
+                        const f2_t q = f2_make(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
+                        l2[e & 1] = f2_add(l2[e & 1], q);
+                        const f2_t y = f2_mul(q, w);
+                        pk[8 * g + e] = pack_f16(f2_lo(y), f2_hi(y));
                     }
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                l2[0] = f2_add(l2[0], l2[1]);
+                l += f2_lo(l2[0]) + f2_hi(l2[0]);
                 // P's buffer was last read by the product of tile i - 2
                 if (i >= 2 && alive) alive = wait(pv_done + pb, (uint32_t)(i / 2 - 1) & 1u, b.ws, 23);
                 __syncwarp();
@@ -1291,33 +1321,42 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 uint32_t o[32];
                 tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)c, o);
                 tmem_wait_ld();
-                if (live && alive) {
-                for (int k = 0; k < bad; ++k)  // channels of NaN values that this row sees (listed tiles only, a few)
-                    for (int e = max(nan_key0[k], lo); e <= min(nan_key0[k] + kKeyTile - 1, hi); ++e) {
-                        const int page = b.table[(size_t)seg.seq * b.max_pages + e / b.page];
-                        if (page < 0 || page >= b.num_pages) continue;
-                        const uint8_t *src = p.v + (((size_t)page * b.Hkv + seg.head) * b.page + e % b.page) * D + c;
+                if (live && alive)
+                    for (int k = 0; k < bad; ++k)  // channels of NaN values that this row sees (noted tiles only, a few)
+                        for (int e = max(nan_key0[k], lo); e <= min(nan_key0[k] + kKeyTile - 1, hi); ++e) {
+                            const int page = b.table[(size_t)seg.seq * b.max_pages + e / b.page];
+                            if (page < 0 || page >= b.num_pages) continue;
+                            const uint8_t *src = p.v + (((size_t)page * b.Hkv + seg.head) * b.page + e % b.page) * D + c;
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if ((src[x] & 0x7f) == 0x7f) o[x] = 0x7fc00000u;
-                    }
-                if (is_whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + place + c);
+                            for (int x = 0; x < 32; ++x)
+                                if ((src[x] & 0x7f) == 0x7f) o[x] = 0x7fc00000u;
+                        }
+                // through shared memory, so that a store covers whole lines: row r's 16-byte piece x at x ^ (r & 7)
+                __syncwarp();
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t w[4];
+                for (int x = 0; x < 8; ++x) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16(__uint_as_float(o[8 * x + 2 * e]) * o_scale, __uint_as_float(o[8 * x + 2 * e + 1]) * o_scale);
-                        dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(slot + 4 * kWideRows + (size_t)r * D + c);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-                }
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = is_whole ? __float_as_uint(__uint_as_float(o[4 * x + e]) * o_scale) : o[4 * x + e];
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {  // four rows at a time, eight lanes each
+                    const int rr = 4 * k + (lane >> 3), x = lane & 7, at = warp * 32 + rr;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((x ^ (rr & 7)) << 4));
+                    if (at < seg.rows && alive) {
+                        if (is_whole) {
+                            const int gr = seg.row + at;
+                            *reinterpret_cast<uint2 *>(p.out + ((size_t)(seg.row0 + gr / G) * b.H + seg.head * G + gr % G) * D + c + 4 * x) =
+                                make_uint2(pack_bf16(__uint_as_float(w.x), __uint_as_float(w.y)),
+                                           pack_bf16(__uint_as_float(w.z), __uint_as_float(w.w)));
+                        } else {
+                            *reinterpret_cast<uint4 *>(slot + 4 * kWideRows + (size_t)at * D + c + 4 * x) = w;
+                        }
+                    }
+                }
             }
             if (tid == 0 && !is_whole && seg.part == 0) plans[cta] = {seg.parts, seg.rows, seg.row0, seg.row * 64 + seg.head};
             tc_fence_before();
@@ -1354,25 +1393,24 @@ rglru_status launch_join(const AttendArgs &p, int grid, cudaStream_t stream)
 }
 
 template <int D>
-rglru_status launch(AttendArgs p, cudaStream_t stream)
+rglru_status launch(const AttendArgs &p, cudaStream_t stream)
 {
     using C = Cfg<D>;
     using W = WideCfg<D>;
     static PerDeviceFlag flag, wide_flag;
-    rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_kernel<D>), C::kSmem, flag);
-    if (st != RGLRU_OK) return st;
     CUtensorMap tm_k, tm_v;
     if (!encode_pool(&tm_k, p.k, p.b) || !encode_pool(&tm_v, p.v, p.b)) return RGLRU_ERR_CUDA;
-    // Sequences with more than two 16-row units go to the 128-row kernel: a unit's tile takes about as long there for all
-    // 128 rows as here for 16.  The 16-row kernel runs in any case: a batch may hold short runs beside long ones.
-    const bool wide = (int64_t)p.b.max_new * (p.b.H / p.b.Hkv) > 2 * kRowTile;
-    p.few = wide ? 2 * kRowTile : INT32_MAX;
-    const int grid = kSms * C::kCtasPerSm;
-    rglru_paged_attention_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p, tm_k, tm_v);
-    if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
-    st = launch_join<D, kRowTile>(p, grid, stream);
-    if (st != RGLRU_OK || !wide) return st;
-    st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_wide_kernel<D>), W::kSmem, wide_flag);
+    // A tile takes the 128-row kernel about 1.3 us an SM whatever its rows, the 16-row one 0.9: from three units of 16 rows on the
+    // first is ahead.  Short runs in the same batch go along with it (a second launch and its join cost 6 us).
+    if ((int64_t)p.b.max_new * (p.b.H / p.b.Hkv) <= 2 * kRowTile) {
+        const rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_kernel<D>), C::kSmem, flag);
+        if (st != RGLRU_OK) return st;
+        const int grid = kSms * C::kCtasPerSm;
+        rglru_paged_attention_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p, tm_k, tm_v);
+        if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
+        return launch_join<D, kRowTile>(p, grid, stream);
+    }
+    const rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_wide_kernel<D>), W::kSmem, wide_flag);
     if (st != RGLRU_OK) return st;
     rglru_paged_attention_wide_kernel<D><<<kSms, kWideThreads, W::kSmem, stream>>>(p, tm_k, tm_v);
     if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
@@ -1401,7 +1439,7 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
 {
     const AttendArgs p = {{rows, S, H, Hkv, head_dim, page_size, num_pages, max_pages, max_new, max_total, cu_tokens,
                            ctx_len, block_table, static_cast<WsHeader *>(workspace)},
-                          window, 0, scale, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
+                          window, scale, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
                           static_cast<const uint8_t *>(v_cache), k_scale, v_scale, static_cast<__nv_bfloat16 *>(out)};
     const size_t need = rglru_paged_attention_workspace_size(H, Hkv, head_dim);
     const rglru_status c = paged::check_batch(p.b, k_cache, k_scale, v_cache, v_scale, workspace_bytes, need);
