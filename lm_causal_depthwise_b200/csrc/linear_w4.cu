@@ -298,7 +298,6 @@ struct Tc {
     static constexpr int kBox = NP * 128;                  // x: 64 k
     static constexpr int kX = 2 * kBox;                    // x of a block
     static constexpr int sums(int M) { return kTcN * M * 4; }
-    static constexpr int smem(int blocks, int M) { return blocks * kX + sums(M) + 1024; }
     static constexpr int max_blocks(int M) { return (226 * 1024 - sums(M) - 1024) / kX; }
 };
 
@@ -647,12 +646,16 @@ rglru_status launch_tc(const W4Args &p, cudaStream_t stream)
         const long long cost = ((long long)(tiles + n - 1) / n) * (share + 3 + (share > h ? 2 * share : 0));
         if (best < 0 || cost < best) best = cost, cluster = c, clusters = n, held = h;
     }
+    // All of the SM's shared memory, whatever the boxes need: two CTAs on an SM would take turns with TMEM, and with two
+    // clusters (or another kernel that waits for its neighbours) each could hold what the other's peers wait for.
+    constexpr int kSmem = 226 * 1024;
     static PerDeviceFlag flag;
-    const rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_linear_w4_tc_kernel<NP, kVec>), 227 * 1024 - 1024, flag);
+    const rglru_status st =
+        set_smem_limit_once(reinterpret_cast<const void *>(rglru_linear_w4_tc_kernel<NP, kVec>), kSmem, flag);
     if (st != RGLRU_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * cluster)), cfg.blockDim = dim3(kTcThreads), cfg.stream = stream;
-    cfg.dynamicSmemBytes = C::smem(held, p.M);
+    cfg.dynamicSmemBytes = kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)cluster, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;

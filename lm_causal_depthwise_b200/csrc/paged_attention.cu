@@ -55,10 +55,11 @@ struct Cfg {
 constexpr int kMeta = 8;  // k of tile t + kSlots - 1 takes the slot of v of tile t or a later one
 
 struct Plan {  // the unit that begins in a CTA's piece and does not end there: its parts, rows and first row's place
-    int parts, rows, row0, row_head;  // row_head: first row (token * G + head in group) * 64 + key/value head
+    short parts, rows;
+    int row0, row, head;  // the sequence's first row; the unit's first (token * G + head in group), its key/value head
 };
-// Workspace: header, plans, then partial results, R rows each: m, mv, l, pad (float4) and O [R][D].  The 16-row kernel has two a
-// CTA (slot 2 c: a unit begun in an earlier CTA; 2 c + 1: one begun here), the 128-row kernel one.
+// Workspace: header, plans, then partial results, R rows each: m, mv, l, pad (float4) and O [R][D].  The 16-row
+// kernel has two a CTA (slot 2 c: a unit begun in an earlier CTA; 2 c + 1: one begun here), the 128-row kernel one.
 constexpr int kWideRows = 128;
 constexpr size_t kPlanBytes = (size_t)kMaxCtas * sizeof(Plan);
 __host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size_t)rows * (4 + D); }
@@ -215,7 +216,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
     const int n_ctas = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles), cta = blockIdx.x;
     Plan *plans = reinterpret_cast<Plan *>(reinterpret_cast<char *>(b.ws) + kWsHeaderBytes);
     if (cta >= n_ctas) {
-        if (tid == 0) plans[cta] = {0, 0, 0, 0};
+        if (tid == 0) plans[cta] = {0, 0, 0, 0, 0};
         return;
     }
     const long long begin = piece_begin(total, cta, n_ctas), end = piece_begin(total, cta + 1, n_ctas);
@@ -344,7 +345,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
     // ---------------------------------------------------------------- consumers
     const int quad = lane >> 2, j = lane & 3;
     float *parts = reinterpret_cast<float *>(reinterpret_cast<char *>(b.ws) + kWsHeaderBytes + align_up_d(kPlanBytes, 256));
-    Plan plan = {0, 0, 0, 0};
+    Plan plan = {0, 0, 0, 0, 0};
     const int kq = quad & 1 ? quad ^ 4 : quad;                 // this thread's key in an 8-key tile (row of k)
     const int je = 2 * j, jo = (2 * j + 1) ^ 4;                // keys of the score columns 2j, 2j + 1 (rows of v)
     const int k_off = (warp * 16 + kq) * 128 + ((j ^ kq) << 4);
@@ -386,10 +387,12 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            int e = min(100, max(-100, (int)(top >> 23) - 127 - 13));
+            int e = max(-126, (int)(top >> 23) - 127 - 13);
             if (top == 0) e = 0;
             const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-            if (warp == 0 && j == 0) qscale[r] = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+            if (warp == 0 && j == 0)  // a row with an infinity or NaN is NaN
+                qscale[r] = top == 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                               : p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
             if (warp < kKb) {
                 const uint4 v0 = live ? src[warp * 8] : make_uint4(0, 0, 0, 0), v1 = live ? src[warp * 8 + 1] : make_uint4(0, 0, 0, 0);
                 const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
@@ -620,7 +623,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
             const bool whole = unit_first && last;
             float *slot = parts + ((size_t)cta * 2 + (unit_first ? 1 : 0)) * part_floats(kRowTile, D);
             if (!whole && unit_first)  // the unit began here and goes on: the later CTAs with a part of it
-                plan = {piece_of(total, end + mt.left - 1, n_ctas) - cta + 1, urows, row0, urow * 64 + head};
+                plan = {(short)(piece_of(total, end + mt.left - 1, n_ctas) - cta + 1), (short)urows, row0, urow, head};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = quad + 8 * h;
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
     sm100::griddep_wait();
     int have[2], inc[2];
     {
-        Plan pl = {0, 0, 0, 0};
+        Plan pl = {0, 0, 0, 0, 0};
         if (tid < n) list[tid] = pl = plans[tid];
         have[0] = pl.parts > 1 && pl.parts <= kFewParts ? pl.rows : 0;
         have[1] = pl.parts > kFewParts ? pl.rows * kSlices : 0;
@@ -725,8 +728,8 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
         return parts + (R == kRowTile ? (size_t)(c + k) * 2 + (k == 0) : (size_t)(c + k)) * part_floats(R, D);
     };
     auto out_row = [&](const Plan &pl, int r) {
-        const int row = (pl.row_head >> 6) + r, head = pl.row_head & 63;
-        return p.out + ((size_t)(pl.row0 + row / G) * b.H + head * G + row % G) * D;
+        const int row = pl.row + r;
+        return p.out + ((size_t)(pl.row0 + row / G) * b.H + pl.head * G + row % G) * D;
     };
 
     for (int item = warp * gridDim.x + blockIdx.x; item < total[0]; item += gridDim.x * kWarps) {
@@ -903,7 +906,8 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     __shared__ uint64_t k_full[kRing], k_free[kRing], rv_full[kRing], rv_free[kRing], v_full[2], v_free[2];
     __shared__ uint64_t q_full, s_full, s_free, p_full[2], pv_done[2], drain[2];
     __shared__ uint32_t tmem_holder;
-    __shared__ int scan[kWideThreads / 32], nan_count, nan_key0[kNanTiles];
+    __shared__ long long scan[kWideThreads / 32];
+    __shared__ int nan_count, nan_key0[kNanTiles];
     __shared__ Segment seg_s;
     const Batch &b = p.b;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = b.H / b.Hkv, cta = blockIdx.x, n_ctas = gridDim.x;
@@ -926,26 +930,32 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     }
     // this thread's sequences and the units before them
     const int per = (b.S + kWideThreads - 1) / kWideThreads, s0 = min(b.S, tid * per), s1 = min(b.S, s0 + per);
-    int mine = 0;
+    long long mine = 0;
     for (int i = s0; i < s1; ++i) mine += wide_units(p, paged::load_seq(b, i));
-    int inc = mine;
+    long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
     }
     if (lane == 31) scan[warp] = inc;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int units = 0, before = inc - mine;
+    long long all = 0, before = inc - mine;
     for (int w = 0; w < kWideThreads / 32; ++w) {
         if (w < warp) before += scan[w];
-        units += scan[w];
+        all += scan[w];
+    }
+    // More units than the rows hold: sequences that overlap, which no batch has.
+    int units = (int)all;
+    if (all > (long long)b.H * b.rows / kWideRows + (long long)b.S * b.Hkv) {
+        units = 0;
+        paged::record_invalid(b.ws);
     }
     const uint32_t tmem = tmem_holder;
     const int whole = units / n_ctas * n_ctas, rest = units - whole, cuts = rest > 0 ? n_ctas / rest : 1;
-    if (tid == 0) plans[cta] = {0, 0, 0, 0};
+    if (tid == 0) plans[cta] = {0, 0, 0, 0, 0};
 
     int n = 0;          // tiles done before this segment: the phase of every barrier
     bool alive = true;
@@ -957,7 +967,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
         }
         __syncthreads();  // the last segment is done with
         if (unit >= before && unit < before + mine) {
-            int at = before;
+            int at = (int)before;
             for (int i = s0; i < s1; ++i) {
                 const paged::Seq s = paged::load_seq(b, i);
                 const int u = wide_units(p, s);
@@ -1173,11 +1183,11 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
 #pragma unroll
                     for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7f800000u, w[x] & 0x7f800000u));
                 }
-                int e = min(100, max(-100, (int)(top >> 23) - 127 - 7));
+                int e = max(-126, (int)(top >> 23) - 127 - 7);
                 if (top == 0) e = 0;
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
                 qs = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-                if (top == 0x7f800000u) qs = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row: codes saturate
+                if (top == 0x7f800000u) qs = __uint_as_float(0x7fc00000u);  // as above (the codes saturate)
 #pragma unroll 2
                 for (int g = 0; g < D / 32; ++g) {  // 32 channels: 8 columns of each term
                     uint32_t hi[8], lo_[8];
@@ -1282,19 +1292,22 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 uint32_t pk[32];
                 f2_t l2[2] = {f2_splat(0.f), f2_splat(0.f)};
                 const float vz = finite_or_0(mv);
-                const f2_t minus = f2_splat(-mz);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    // below 2^126: a key whose 2^(s - m) underflows stays 0
-                    const f2_t w = f2_splat(ex2_approx(fminf(lv[g] - vz, 126.f)));
+                    // P = 2^(s - m + d), l sums 2^(s - m).  Where d is above 100 (values 2^100 apart), 2^(s - m) would
+                    // underflow under a P that counts: then the exponential is taken at s - m + d - 100, at most 2^-92.
+                    const float d = lv[g] - vz, over = fmaxf(0.f, d - 100.f);
+                    const f2_t w = f2_splat(ex2_approx(d - over)), minus = f2_splat(over - mz);
+                    f2_t lg[2];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const f2_t x = f2_add(v[8 * g + e], minus);
                         const f2_t q = f2_make(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
-                        l2[e & 1] = f2_add(l2[e & 1], q);
+                        lg[e & 1] = e < 2 ? q : f2_add(lg[e & 1], q);
                         const f2_t y = f2_mul(q, w);
                         pk[8 * g + e] = pack_f16(f2_lo(y), f2_hi(y));
                     }
+                    l2[g & 1] = f2_fma(f2_add(lg[0], lg[1]), f2_splat(ex2_approx(-over)), l2[g & 1]);
                 }
                 l2[0] = f2_add(l2[0], l2[1]);
                 l += f2_lo(l2[0]) + f2_hi(l2[0]);
@@ -1358,7 +1371,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     }
                 }
             }
-            if (tid == 0 && !is_whole && seg.part == 0) plans[cta] = {seg.parts, seg.rows, seg.row0, seg.row * 64 + seg.head};
+            if (tid == 0 && !is_whole && seg.part == 0) plans[cta] = {(short)seg.parts, (short)seg.rows, seg.row0, seg.row, seg.head};
             tc_fence_before();
         }
         n += tiles;
@@ -1446,6 +1459,10 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
     if (c != RGLRU_OK) return c;
     if ((int64_t)num_pages * Hkv * page_size > INT32_MAX) return RGLRU_ERR_UNSUPPORTED;  // rows of a tensor map
     if (!args::al16(q) || !args::al16(out) || window < 1 || !(scale > 0.f) || scale > 1e30f) return RGLRU_ERR_INVALID_ARG;
+    // counts of rows and of a CTA's tiles stay below 2^31
+    const int64_t span = (int64_t)(max_total < (int64_t)window + max_new ? max_total : (int64_t)window + max_new) / kKeyTile + 2;
+    const int64_t units = (int64_t)rows * H / kRowTile + (int64_t)S * Hkv;
+    if ((int64_t)rows * H > INT32_MAX || units / kSms + 1 > INT32_MAX / span) return RGLRU_ERR_UNSUPPORTED;
     const size_t pool = (size_t)num_pages * Hkv, act = (size_t)rows * H * head_dim * 2;
     const args::Span in[] = {args::span(q, act),
                              args::span(cu_tokens, ((size_t)S + 1) * 4),

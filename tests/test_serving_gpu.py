@@ -9,9 +9,12 @@ Bars, from the arithmetic.  A rounding is off by at most half a step: bf16 2^-8 
              (a tensor core may truncate), which sum |s q x| bounds.
   append     the angle is a turn in fp32 (2^-25 of it, times 2 pi) and its sine and cosine 2^-23; three
              roundings of 2^-24 follow: 1e-6 (|x1| + |x2|) holds them.  Values are copies: codes of v exact.
-  attention  scores: head_dim / 16 + 8 sequential additions off by 2^-23 of sum |q k| scale each; q enters as f16 after an exact
-             power of two (it has 8 bits), k exactly; the exponential and its argument 2^-18; a probability
-             enters the second product as f16 (2^-11), and the sums are fp32: relative to sum p |v|.
+  attention  scores: head_dim / 16 + 8 sequential additions off by 2^-23 of sum |q k| scale each; q enters exactly, as
+             f16 after a power of two (it has 8 bits), or, in calls with more than 32 rows a sequence and key head, as
+             two e4m3 terms, exact down to 2^-9 of the row's largest value and off by 2^-17 of that below: of normal
+             values fewer than one in a hundred, so at most 2^-17 * 4 / 100 of sum |q k| * 3, far inside the additions'
+             2^-18 and more; k enters exactly; the exponential and its argument 2^-18; a probability enters the second
+             product as f16 (2^-11), and the sums are fp32: relative to sum p |v|.
 A scale is a power of two: it may differ only where the largest magnitude is within those errors of the border.
 """
 import numpy as np
@@ -161,6 +164,35 @@ def test_linear_w4(M, N, K, group, a_group):
     (64, 300, 5120, 64, 256, True), (2, 4099, 160, 32, 32, True), (20, 40, 20480, 128, 128, True), (4, 9, 192, 64, 32, True)])
 def test_linear_w4_sizes(M, N, K, group, a_group, bias):
     _check_w4(np.random.default_rng(N + K), M, N, K, group, a_group, bias)
+
+
+@pytest.mark.parametrize("M,N,K,group,a_group", [
+    (64, 70, 20480, 128, 128), (20, 20001, 128, 128, 0), (48, 20001, 288, 32, 32), (64, 20001, 1280, 64, 0),
+    (64, 4300, 12320, 32, 0), (16, 9000, 288, 32, 0), (1, 40, 20480, 64, 128)])
+def test_linear_w4_rounds_and_passes(M, N, K, group, a_group):
+    """More outputs than the clusters take at once, more of x than shared memory holds, long sums for few rows."""
+    _check_w4(np.random.default_rng(M + N + K), M, N, K, group, a_group)
+
+
+def test_linear_w4_repeats_beside_another_stream():
+    """Sums over a cluster in rank order: the same bits each time, also with other projections on a second stream."""
+    rng = np.random.default_rng(7)
+    cases = []
+    for M, N, K in ((40, 1000, 2560), (64, 3000, 384), (20, 500, 5120)):
+        A, _, W, s, b, _ = (t if t is None or isinstance(t, np.ndarray) else t.to(dev) for t in _w4_case(rng, M, N, K, 128, 0))
+        cases.append((A, W, s, b))
+    ref = [api.linear_w4(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for st in streams:
+            with torch.cuda.stream(st):
+                outs.append([api.linear_w4(*c) for c in cases])
+    torch.cuda.synchronize()
+    for o in outs:
+        for a, r in zip(o, ref):
+            assert torch.equal(a, r)
 
 
 def test_linear_w4_every_code_at_every_place():
@@ -404,6 +436,116 @@ def test_paged_attention_uneven_batch():
     _check_attend(World(11, [6000, 0, 17, 3, 900], [2, 1, 0, 5, 1], 8, 2, 128, 32, pad=2), 5000)
 
 
+@pytest.mark.parametrize("ctx,new,H,Hkv,D,page,window,kw", [
+    ([6000], [5], 8, 1, 128, 64, api.FULL_WINDOW, {}),                # one unit over many SMs
+    ([5000, 3], [5, 1], 8, 1, 256, 16, 4096, {}),
+    ([50 + i for i in range(40)], [33] * 40, 16, 1, 128, 32, 64, {}),  # whole units and cut ones
+    ([900, 100, 0, 77, 300], [1, 64, 0, 1, 130], 4, 2, 256, 64, 200, {}),  # single tokens beside chunks
+    ([70, 0, 257], [1, 1, 1], 64, 1, 128, 32, 100, {}),               # single tokens, many heads to a key head
+    ([70, 400], [3, 1], 6, 2, 128, 16, 90, dict(max_new=500, max_total=1000)),  # bounds above the lengths
+    ([0, 63, 64], [64, 65, 1], 3, 1, 256, 128, 64, {})])
+def test_paged_attention_chunks(ctx, new, H, Hkv, D, page, window, kw):
+    w = World(len(ctx) + D, ctx, new, H, Hkv, D, page, pad=1)
+    if kw:
+        w.table = np.pad(w.table, ((0, 0), (0, kw["max_total"] // page + 1 - w.table.shape[1])), constant_values=-7)
+    got = _check_attend(w, window, **kw)
+    assert torch.equal(_attend(w, window, **kw)[0], got)
+
+
+def test_paged_attention_chunks_with_far_apart_scales_and_queries():
+    """As below, for chunks: scales up to 2^130 apart, the heavy probability on the small values or not, sharp rows,
+    large, small and zero rows."""
+    w = World(42, [300, 0], [20, 40], 4, 1, 256, 16)
+    w.q = (w.q.float() * 8).to(bf)
+    _check_attend(w, api.FULL_WINDOW)
+    w.vs[:] = np.exp2(w.rng.integers(-100, 31, w.vs.shape).astype(float))
+    _check_attend(w, api.FULL_WINDOW)
+    _check_attend(w, 33, scale=1e-3)
+    w = World(43, [77], [40], 2, 1, 128, 16)
+    q = w.q.float().view(40, 2, 128)
+    q[2] *= 1e-20
+    q[3] = 0
+    q[5] *= 2.0 ** -110
+    w.q = q.view(40, 256).to(bf)
+    _check_attend(w, api.FULL_WINDOW, scale=1.0)
+
+
+def test_paged_attention_value_scales_beyond_a_float_exponent():
+    """A key whose probability is below 2^-126 counts when its values are 2^146 times the others': single tokens, chunks."""
+    for new in (1, 40):
+        w = World(44, [100], [new], 1, 1, 128, 16)
+        w.ks[:] = 2.0 ** -8
+        w.k[:], w.vs[:] = 0, 2.0 ** -90
+        w.v = np.where(w.v == 0, 1.0, w.v)
+        q = torch.zeros(new, 128)
+        q[:, 0] = 1.0
+        w.q = q.to(bf)
+        # position 3's score is -140 (log2 units), its page's values 2^146 times larger; the other scores are 0
+        far = w.table[0, 0]
+        w.k[far, 0, :, 0] = -448
+        w.k[far, 0, 3, 0] = -256
+        w.vs[far] = 2.0 ** 56
+        scale = 140 * np.log(2)
+        got, ws = _attend(w, api.FULL_WINDOW, scale)
+        want, size, smax = O.attention(_np(w.q).reshape(w.rows, 1, 128), w.cu, w.ctx, w.table, w.k, w.ks, w.v, w.vs,
+                                       api.FULL_WINDOW, float(np.float32(scale)))
+        # the argument of that key's exponential is 140 with 24 bits: 2^-17 and log2 e's rounding as much
+        rel = 2.0 ** -11 + 2.0 ** -15 + 2 * 16 * 2.0 ** -23 * smax
+        _within(_np(got).reshape(want.shape), want, 2.0 ** -8 * np.abs(want) + rel[..., None] * size, "far key")
+        near = O.attention(_np(w.q).reshape(w.rows, 1, 128), w.cu, w.ctx, w.table, w.k, w.ks, w.v,
+                           np.where(w.vs > 1, 0, w.vs), api.FULL_WINDOW, scale)[0]
+        assert (np.abs(want - near) > 2.0 ** -6 * np.abs(want)).mean() > 0.9      # the key does count
+
+
+def test_paged_attention_rows_of_inf_and_nan_and_large_queries():
+    """An infinity or NaN in a query makes its row NaN and no other; queries up to the type's range keep their bits."""
+    for new in (6, 40):
+        w = World(45, [50], [new], 2, 1, 128, 16)
+        clean = w.q.clone()
+        ref = _attend(w, api.FULL_WINDOW)[0].view(new, 2, 128)
+        w.q = clean.clone().view(new, 2, 128)
+        w.q[1, 0, 5], w.q[3, 1, 0], w.q[4, 1, 9] = float("nan"), float("inf"), -float("inf")
+        w.q = w.q.view(new, 256)
+        got = _attend(w, api.FULL_WINDOW)[0].view(new, 2, 128)
+        for t in range(new):
+            for h in range(2):
+                if (t, h) in ((1, 0), (3, 1), (4, 1)):
+                    assert got[t, h].isnan().all()
+                else:
+                    assert torch.equal(got[t, h], ref[t, h])
+        for p in (120, -120):                                  # undone by the scales
+            w.q, ks = (clean.float() * 2.0 ** p).to(bf), w.ks.copy()
+            w.ks = w.ks * 2.0 ** -(p // 2)
+            big = _check_attend(w, api.FULL_WINDOW, scale=128 ** -0.5 * 2.0 ** -(p // 2)).view(new, 2, 128)
+            w.ks = ks
+            # the same bits, where no query leaves bf16's normal range: times 2^-120, those below 2^-6 become
+            # multiples of 2^-133 and are other inputs
+            assert p < 0 or torch.equal(big, ref)
+
+
+def test_paged_attention_query_outlier_in_chunks():
+    """One channel 2^12 times the others: what two e4m3 terms lose of the small ones, 2^-17 of the largest a channel."""
+    w = World(46, [60], [40], 2, 1, 128, 16)
+    q = w.q.float().view(40, 2, 128)
+    q[..., 7] = 2.0 ** 12 * (1 + torch.rand(40, 2))
+    w.q = q.view(40, 256).to(bf)
+    got = _attend(w, api.FULL_WINDOW)[0]
+    qn = _np(w.q).reshape(40, 2, 128)
+    want, size, smax = O.attention(qn, w.cu, w.ctx, w.table, w.k, w.ks, w.v, w.vs, api.FULL_WINDOW, 128 ** -0.5)
+    kk = (np.abs(w.k) * w.ks[:, :, None, None]).sum(-1).max()
+    loss = 2.0 ** -17 * np.abs(qn).max(-1) * kk * 128 ** -0.5       # of a score; twice that in a probability's exponent
+    rel = 2.0 ** -11 + 2 * 16 * 2.0 ** -23 * smax + 2.0 ** -18
+    _within(_np(got).reshape(want.shape), want, 2.0 ** -8 * np.abs(want) + (rel + np.expm1(2 * loss))[..., None] * size, "outlier")
+
+
+def test_paged_attention_overlapping_sequences_are_refused_on_the_device():
+    w = World(47, [0, 0, 0, 0, 0], [40, 0, 0, 0, 0], 64, 1, 128, 16)
+    cu = torch.tensor([0, 40, 0, 40, 0, 40], dtype=torch.int32, device=dev)
+    w.table[:] = w.table[0]
+    got, ws = _attend(w, 30, cu_tokens=cu)
+    assert api.device_status(ws) == api.ERR_INVALID_ARG and (got == 55).all()
+
+
 def test_paged_attention_sharp_and_far_apart_scales():
     """Scores large enough that one key takes all; pages whose value scales are 2^40 apart, the heavy
     probability on the small ones."""
@@ -616,6 +758,61 @@ def test_serving_steps_eager_and_captured():
         # h2 = y + h: the 8-bit and bf16 roundings of the step enter y (of size 2^-9 * 8 * sqrt(N) ~ 0.1); a code that
         # rounds the other way moves a value by 2^-4, one of hundreds in a sum: 2^-6 of the row's rms is far above that
         _within(_np(got), want, 2.0 ** -7 * np.abs(want) + 2.0 ** -6, "step")
+
+
+def test_chunks_captured_and_replayed_with_other_lengths():
+    """Append and attention of chunks as one graph, replayed while the lengths and the table change in place."""
+    D, H, page, rows = 128, 4, 16, 96
+    ws = api.new_workspace(api.paged_attention_workspace_size(H, 1, D))
+    worlds = [World(50 + i, c, n, H, 1, D, page) for i, (c, n) in enumerate((([0, 20, 5], [40, 50, 6]), ([90, 0, 33], [1, 95, 0]),
+                                                                           ([0, 0, 0], [32, 32, 32])))]
+    pages = max(x.P for x in worlds)
+    cache = api.paged_cache(pages, 1, page, D)
+    batch = api.PagedBatch(torch.zeros(4, dtype=torch.int32, device=dev), torch.zeros(3, dtype=torch.int32, device=dev),
+                           torch.full((3, 10), -7, dtype=torch.int32, device=dev), 96, 160)
+    qkv = torch.zeros(rows, (H + 2) * D, dtype=bf, device=dev)
+    q, o = (torch.full((rows, H * D), 55.0, dtype=bf, device=dev) for _ in range(2))
+
+    def call():
+        api.paged_append(qkv, batch, cache, q_out=q, workspace=ws)
+        api.paged_attention(q, batch, cache, window=50, out=o, workspace=ws)
+
+    def fill(x):
+        batch.cu_tokens.copy_(torch.from_numpy(x.cu))
+        batch.ctx_len.copy_(torch.from_numpy(x.ctx.astype(np.int32)))
+        batch.block_table.fill_(-7)
+        batch.block_table[:, :x.table.shape[1]].copy_(torch.from_numpy(x.table))
+        c = x.cache()
+        for d, s in zip((cache.k, cache.k_scale, cache.v, cache.v_scale), (c.k, c.k_scale, c.v, c.v_scale)):
+            d[:x.P].view(torch.uint8).copy_(s.view(torch.uint8))
+        qkv[:x.rows].copy_(x.qkv)
+        q.fill_(55.0), o.fill_(55.0)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for x in worlds:
+        fill(x)
+        call()
+        eager = [t.clone() for t in (q, o, cache.k.view(torch.uint8), cache.v.view(torch.uint8))]
+        fill(x)
+        g.replay()
+        for a, b in zip((q, o, cache.k.view(torch.uint8), cache.v.view(torch.uint8)), eager):
+            assert torch.equal(a, b)
+        assert api.device_status(ws) == api.OK and (o[x.rows:] == 55).all()
+        y = _np(x.qkv).reshape(x.rows, -1)
+        got_q = _np(q)[:x.rows].reshape(x.rows, H, D)
+        new = O.append(y, x.cu, x.ctx, x.table, x.k, x.ks, x.v, x.vs, H)[1]
+        kc, ks = _np(cache.k)[:x.P], _np(cache.k_scale)[:x.P]
+        np.testing.assert_array_equal(_np(cache.v)[:x.P], new["v"][0])
+        want, size, smax = O.attention(got_q, x.cu, x.ctx, x.table, kc, ks, new["v"][0], new["v"][1], 50, D ** -0.5)
+        rel = 2.0 ** -11 + 2 * (D / 16 + 8) * 2.0 ** -23 * smax + 2.0 ** -18
+        _within(_np(o)[:x.rows].reshape(want.shape), want, 2.0 ** -8 * np.abs(want) + rel[..., None] * size, "chunks")
 
 
 def test_operators_on_another_stream_and_two_at_once():
