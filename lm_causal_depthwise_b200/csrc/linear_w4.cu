@@ -646,16 +646,19 @@ rglru_status launch_tc(const W4Args &p, cudaStream_t stream)
         const long long cost = ((long long)(tiles + n - 1) / n) * (share + 3 + (share > h ? 2 * share : 0));
         if (best < 0 || cost < best) best = cost, cluster = c, clusters = n, held = h;
     }
-    // All of the SM's shared memory, whatever the boxes need: two CTAs on an SM would take turns with TMEM, and with two
-    // clusters (or another kernel that waits for its neighbours) each could hold what the other's peers wait for.
-    constexpr int kSmem = 226 * 1024;
+    // At least half of the SM's shared memory: two CTAs on an SM would take turns with TMEM, and of two clusters (or one and
+    // another kernel whose CTAs wait for each other; those take 170 KB or more) each could hold what the other's peers
+    // wait for.  Not all of it: the rest is L1, and 37 rows of 12289 x 4096 took 44 us instead of 38.
+    constexpr int kSmem = 226 * 1024, kLeast = 115 * 1024;
+    static_assert(2 * (kLeast + 1024) > 228 * 1024, "one CTA an SM");
     static PerDeviceFlag flag;
     const rglru_status st =
         set_smem_limit_once(reinterpret_cast<const void *>(rglru_linear_w4_tc_kernel<NP, kVec>), kSmem, flag);
     if (st != RGLRU_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * cluster)), cfg.blockDim = dim3(kTcThreads), cfg.stream = stream;
-    cfg.dynamicSmemBytes = kSmem;
+    const int need = held * C::kX + C::sums(p.M) + 1024;
+    cfg.dynamicSmemBytes = need < kLeast ? kLeast : need;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)cluster, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
