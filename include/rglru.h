@@ -554,7 +554,9 @@ RGLRU_API rglru_status rglru_add_rmsnorm_e4m3(int M, int N, int group, const voi
  *   value); bias [N] fp32 or NULL; out [M, N] bf16.
  * 1 <= M <= 64 (more rows: RGLRU_ERR_UNSUPPORTED; rglru_linear is the call for
  * those), any N up to 2^20, K up to 2^20.  The weights' integers and x enter
- * the products exactly, sums are fp32, the output is rounded once.
+ * the products exactly, sums are fp32, the output is rounded once.  There is no
+ * workspace, and no status word: a device-side wait that ran out (2 s, more
+ * than 16 rows only) would leave NaN in the outputs it held up.
  */
 RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group, const void *A, const float *A_scale,
                                        int a_group, const void *W, const void *W_scale, const float *bias, void *out,
@@ -613,8 +615,17 @@ RGLRU_API size_t rglru_paged_attention_workspace_size(int H, int Hkv, int head_d
  * q, out [rows, H * head_dim] bf16 (q as rglru_paged_append gives it); window
  * >= 1 (2^30 or more reaches every position); scale > 0.  Scores, sums and the
  * output's accumulation are fp32; the probabilities enter the second product
- * as f16.  A row with no key (bad pages only) gives zeros.  The workspace is
- * zero-filled once and not shared by calls that can overlap.
+ * as f16.  With max_new * H / Hkv <= 32 q enters the first product exactly; with
+ * more (chunks) as two e4m3 terms, exact for channels down to 2^-9 of the row's
+ * largest and off by at most 2^-17 of it below.  A row with no key (bad pages
+ * only) gives zeros, a row whose q has an infinity or NaN gives NaN.
+ * num_pages * Hkv * page_size and rows * H are below 2^31 (else
+ * RGLRU_ERR_UNSUPPORTED).  Sequences whose rows overlap
+ * are recorded as RGLRU_ERR_INVALID_ARG when they come to more rows than the
+ * call has.  The workspace (up to 20 MB, whatever the batch) is zero-filled once
+ * and not shared by calls that can overlap; a device-side wait that ran out
+ * (2 s) is recorded there as RGLRU_ERR_TIMEOUT, and the rows it held up are not
+ * written.
  */
 RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, int head_dim, int page_size,
                                              int num_pages, int max_pages, int max_new, int max_total, int window,

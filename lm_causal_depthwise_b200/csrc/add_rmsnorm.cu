@@ -4,12 +4,11 @@
 //   y = h * rsqrt(mean_n(h^2) + eps) * weight   as bf16, or as e4m3 with one power-of-two
 //                                               scale for each group of channels (e4m3.cuh)
 //
-// The decoder layer adds the temporal block's output to its input and
-// normalises the sum (channel_pre_norm).  In one kernel the sum is read from
-// registers instead of from memory: 8 bytes per element with a bf16 output (7 with
-// an 8-bit one) against 10 for an addition and rglru_rmsnorm.  h is rounded to bf16
-// before the norm, so that the result is what the two calls give.  The sum of squares, the mean
-// and the scaled row are fp32.
+// The decoder layer adds the temporal block's output to its input and normalises the sum (channel_pre_norm).  In one
+// kernel the sum is read from registers instead of from memory: 8 bytes per element with a bf16 output (7 with an 8-bit
+// one) against 10 for an addition and rglru_rmsnorm.  h is rounded to bf16 before the norm, so that the result is what
+// the two calls give.  The sum of squares, the mean and the scaled row are fp32.  Memory bound: 32768 x 2560 takes
+// 106 us, 6.3 TB/s; a few rows take the launch (4 x 2560: 10 us).
 #include "e4m3.cuh"
 #include "internal.h"
 
@@ -84,7 +83,8 @@ rglru_add_rmsnorm_kernel(int M, int N, int group, const uint4 *__restrict__ x, c
         if (row + (int)gridDim.x < M) load(row + gridDim.x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if ((tid & 31) == 0) part[turn][tid >> 5] = ss;  // two turns: a row's sums are read while the next row's are written
+        // two turns: a row's sums are read while the next row's are written
+        if ((tid & 31) == 0) part[turn][tid >> 5] = ss;
         __syncthreads();
         ss = 0.f;
         for (int k = 0; k < (int)blockDim.x / 32; ++k) ss += part[turn][k];
@@ -120,8 +120,8 @@ rglru_add_rmsnorm_kernel(int M, int N, int group, const uint4 *__restrict__ x, c
 }
 
 template <int VPT, bool kE4m3>
-rglru_status launch_vpt(int M, int N, int group, const void *x, const void *res, const float *w, float eps, void *res_out,
-                        void *out, float *out_scale, cudaStream_t stream)
+rglru_status launch_vpt(int M, int N, int group, const void *x, const void *res, const float *w, float eps,
+                        void *res_out, void *out, float *out_scale, cudaStream_t stream)
 {
     const int threads = ((N / 8 + VPT - 1) / VPT + 31) / 32 * 32;
     // resident threads: 2048 an SM fill it, but the bf16 form with one vector a thread runs better with 1536 (below)
@@ -131,9 +131,11 @@ rglru_status launch_vpt(int M, int N, int group, const void *x, const void *res,
     const auto *wv = reinterpret_cast<const float4 *>(w);
     auto *ro = static_cast<uint4 *>(res_out);
     if (res != nullptr)
-        rglru_add_rmsnorm_kernel<VPT, kE4m3, true><<<grid, threads, 0, stream>>>(M, N, group, xv, rv, wv, eps, ro, out, out_scale);
+        rglru_add_rmsnorm_kernel<VPT, kE4m3, true>
+            <<<grid, threads, 0, stream>>>(M, N, group, xv, rv, wv, eps, ro, out, out_scale);
     else
-        rglru_add_rmsnorm_kernel<VPT, kE4m3, false><<<grid, threads, 0, stream>>>(M, N, group, xv, rv, wv, eps, ro, out, out_scale);
+        rglru_add_rmsnorm_kernel<VPT, kE4m3, false>
+            <<<grid, threads, 0, stream>>>(M, N, group, xv, rv, wv, eps, ro, out, out_scale);
     return cuda_status(cudaGetLastError());
 }
 
@@ -141,9 +143,9 @@ template <bool kE4m3>
 rglru_status launch(int M, int N, int group, const void *x, const void *res, const float *w, float eps, void *res_out,
                     void *out, float *out_scale, cudaStream_t stream)
 {
-    // 32768 x 2560, bf16: one vector a thread and 1536 threads an SM 106 us (97% of the measured bandwidth with the launch), 2048
-    // threads 117, two vectors 113.  The e4m3 form has the maxima's shuffles to hide: two vectors and 2048 threads 111 us, one
-    // vector 123 to 131; 4099 x 4096 27 us against 31.
+    // 32768 x 2560, bf16: one vector a thread and 1536 threads an SM 106 us (97% of the measured bandwidth with the
+    // launch), 2048 threads 117, two vectors 113.  The e4m3 form has the maxima's shuffles to hide: two vectors and 2048
+    // threads 111 us, one vector 123 to 131; 4099 x 4096 25 us against 31.
     if (!kE4m3 && N <= 4096) return launch_vpt<1, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
     if (N <= 2 * 4096) return launch_vpt<2, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
     return launch_vpt<4, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);

@@ -2,17 +2,17 @@
 //
 //   out[m, n] = sum_g s[n, g] * sum_{k in group g} (q[n, k] - 8) * x[m, k] + bias[n]
 //
-// q in 0..15, two to a byte along K (the even k in the low half), s in bf16, x in bf16 or in
-// e4m3 with a scale for each group of channels.  Bound by the weight bytes, N K / 2 and 2 N K / group for the scales, while
-// there are few rows.
+// q in 0..15, two to a byte along K (the even k in the low half), s in bf16, x in bf16 or in e4m3 with a scale for each
+// group of channels.  Bound by the weight bytes, N K / 2 and 2 N K / group for the scales, while there are few rows.
 //
-// Both kernels use the mma m16n8k16 with the weights as the 16-row operand and the
-// rows of x as its 8 columns.  q - 8 is exact in bf16: the nibble is set into the mantissa of 128 (0x4300 | q is
-// 128 + q) and 136 is subtracted, two values an instruction, and the scale multiplies the fp32 sum of a group, so
-// no weight is ever rounded.  A word of eight nibbles k0 .. k7 gives the pairs (k0, k4), (k1, k5),
-// (k2, k6), (k3, k7) by shift and mask alone; x is paired the same way, since the order of a sum's terms is free.
-// Of a block of 128 k (four sub-blocks of 32) thread j of a quad takes word j of each sub-block: an mma never mixes two
-// groups of 32 or more.
+// Both kernels have the weights as the operand of many rows and the rows of x as its columns.  q - 8 is exact in bf16:
+// the nibble is set into the mantissa of 128 (0x4300 | q is 128 + q) and 136 is subtracted, two values an instruction,
+// and the scale multiplies the fp32 sum of a group, so no weight is ever rounded.  A word of eight nibbles k0 .. k7
+// gives the pairs (k0, k4), (k1, k5), (k2, k6), (k3, k7) by shift and mask alone; x is paired the same way, since the
+// order of a sum's terms is free.
+//
+// Measured with the launch: 1 row of 2560 x 2560 9 us and 8 rows (e4m3) of 7680 x 2560 10 us, both the host's time for
+// a call; 37 rows of 12289 x 4096 in groups of 32 38 us.
 #include "e4m3.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -90,10 +90,11 @@ __device__ __forceinline__ void pair_up_e4m3(uint2 x, float s, uint32_t (&r)[4])
 }
 
 // ------------------------------------------------------------------------------------------------ up to 16 rows
-// A CTA takes 16 R outputs, its 8 warps every eighth block of 128 k; the warps' sums meet in shared memory.  A
-// warp's weights come by cp.async into its own ring (1 KB a block and row tile; 16-byte chunk i of row r sits at
-// i ^ (r / 2 % 4), so that the 4-byte reads of a sub-block touch every bank once), its x and scales straight into
-// registers one block ahead.
+// mma m16n8k16, 16 outputs and 8 rows of x.  A CTA takes 16 R outputs, its 8 warps every eighth block of 128 k; the
+// warps' sums meet in shared memory.  Of a block (four sub-blocks of 32 k) thread j of a quad takes word j of each
+// sub-block: an mma never mixes two groups of 32 or more.  A warp's weights come by cp.async into its own ring (1 KB a
+// block and row tile; 16-byte chunk i of row r sits at i ^ (r / 2 % 4), so that the 4-byte reads of a sub-block touch
+// every bank once), its x and scales straight into registers, kAhead blocks ahead.
 constexpr int kWarps = 8, kRing = 4;
 template <int NT, int R>
 struct Few {
@@ -279,16 +280,18 @@ __global__ void __launch_bounds__(kWarps * 32) rglru_linear_w4_kernel(const W4Ar
 }
 
 // ------------------------------------------------------------------------------------------------ more rows or outputs
-// The weights of 128 outputs and 128 k become a bf16 operand in TMEM, once for all rows of x, and the products run on tcgen05
-// (M = 128 outputs, N = rows of x): with mma.sync each warp unpacked, paired and scaled for itself, 613 instructions
-// for 16 outputs and 128 k, and 37 rows of 12289 x 4096 took 53 us.  Unpacked into shared memory the stores and the
-// products' reads of the weights held each other up (a block's products 0.9 us, 0.45 without the stores).
+// The weights of 128 outputs and 128 k become a bf16 operand in TMEM, once for all rows of x, and the products run on
+// tcgen05 (M = 128 outputs, N = rows of x): with mma.sync each warp unpacked, paired and scaled for itself, 613
+// instructions for 16 outputs and 128 k, and 37 rows of 12289 x 4096 took 53 us.  Unpacked into shared memory the
+// stores and the products' reads of the weights held each other up (a block's products 0.9 us, 0.45 without the
+// stores; 46 us).  In TMEM it takes 38 us, 26 of them without the adding of the groups' sums (0.9 us a block in groups
+// of 32: four times 48 columns through registers), which is what bounds it.
 //   warps 0-3    thread = output = TMEM lane: adds a group's sum, times its scale, to fp32 accumulators
 //   warp 4       issues the products: a group at a time into its own TMEM columns
 //   warps 5-12   unpack: a thread has 64 k of one output, read 32 bytes at a time several blocks ahead
-// K is split over the CTAs of a cluster; a CTA keeps its share of x in shared memory as operand boxes (64 k, 128-byte swizzle;
-// taken out of e4m3 there) while it walks over the outputs, 128 a round.  The cluster's sums meet
-// through distributed shared memory, in rank order.
+// K is split over the CTAs of a cluster; a CTA keeps its share of x in shared memory as operand boxes (64 k, 128-byte
+// swizzle; taken out of e4m3 there) while it walks over the outputs, 128 a round.  The cluster's sums meet through
+// distributed shared memory, in rank order.
 constexpr int kTcN = 128, kTcThreads = 13 * 32, kTcUnpack = 8 * 32, kTcStages = 2, kTcAhead = 4;
 constexpr uint32_t kTcColA = 512 - kTcStages * 64;  // unpacked blocks; the groups' sums before them
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -547,8 +550,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
                 }
             }
         }
-        // The cluster's sums of this round: written, then read by warps 0-3.  The other warps pass both barriers of a round at the end of
-        // their next one, and are unpacking it meanwhile.
+        // The cluster's sums of this round: written, then read by warps 0-3.  The other warps pass both barriers of a
+        // round at the end of their next one, and are unpacking it meanwhile.
         __syncwarp();
         if (warp >= 4) {
             if (round > 0) cluster_wait(), cluster_arrive(), cluster_wait();
@@ -633,9 +636,9 @@ template <int NP, bool kVec>
 rglru_status launch_tc(const W4Args &p, cudaStream_t stream)
 {
     using C = Tc<NP>;
-    // The split of K: rounds of the busiest CTA times a round's blocks (and about three blocks' time to end it), over cluster
-    // sizes.  Clusters of several CTAs find room on 132 of the 148 SMs (33 clusters of 4 were resident, the rest of a GPC
-    // does not hold one): one cluster more would run after all others.
+    // The split of K: rounds of the busiest CTA times a round's blocks (and about three blocks' time to end it), over
+    // cluster sizes.  Clusters of several CTAs find room on 132 of the 148 SMs (33 clusters of 4 were resident, the rest
+    // of a GPC does not hold one): one cluster more would run after all others.
     const int tiles = (p.N + kTcN - 1) / kTcN, blocks = (p.K + kBlockK - 1) / kBlockK;
     int cluster = 1, clusters = 1, held = 1;
     long long best = -1;
@@ -698,8 +701,8 @@ extern "C" RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group
     auto log2i = [](int v) { int s = 0; while ((1 << s) < v) ++s; return s; };
     const W4Args p = {M, N, K, log2i(group), A_scale ? log2i(a_group) : 0, A, A_scale, static_cast<const uint8_t *>(W),
                       static_cast<const uint16_t *>(W_scale), bias, static_cast<__nv_bfloat16 *>(out)};
-    // Up to 16 rows the first kernel is as fast or faster at every size measured (16 rows of 12288 x 4096: 35 us both; 8 rows of
-    // 7680 x 2560 13 us against 20; one row of 2560 x 2560 10 against 14).
+    // Up to 16 rows the first kernel is as fast or faster at every size measured (16 rows of 12288 x 4096: 35 us both;
+    // 8 rows of 7680 x 2560 13 us against 20; one row of 2560 x 2560 10 against 14).
     if (M <= 16) return M <= 8 ? launch_few<1>(p, stream) : launch_few<2>(p, stream);
     switch ((M + 15) / 16) {
     case 2: return launch_tc<32>(p, stream);

@@ -1,23 +1,24 @@
 // paged_append.cu -- the new tokens' keys and values into a paged 8-bit cache, rotated on the way.
 //
-// RoPE turns the pairs (x[i], x[i + D/2]) of the query heads and the keys by
-// position * base^(-2i/D); q is written bf16, k and v as e4m3 codes.  A page's
-// scale covers all its slots: the run of tokens that enters a page at its first slot sets it from
-// its own largest magnitude; a run that enters later keeps the larger of the
-// page's scale and its own, and when that raised the scale the older slots are moved to it (an exponent shift,
-// rounded only where it underflows).
+// RoPE turns the pairs (x[i], x[i + D/2]) of the query heads and the keys by position * base^(-2i/D); q is written
+// bf16, k and v as e4m3 codes.  A page's scale covers all its slots: the run of tokens that enters a page at its first
+// slot sets it from its own largest magnitude; a run that enters later keeps the larger of the page's scale and its
+// own, and when that raised the scale the older slots are moved to it (an exponent shift, rounded only where it
+// underflows).
 //
-// Memory bound: 2 (H + 2 Hkv) D bytes read and 2 H D + 2 Hkv D written per token.  A CTA owns one
-// page of one key or value head, so that the page's maximum never leaves it: the run's values stay in registers
-// between the maximum and the rounding.  The query heads need no maximum: other CTAs take a token and 16 channels
-// a thread, and up to five heads with the same sines and cosines, all of their loads in flight at once.
+// Memory bound: 2 (H + 2 Hkv) D bytes read and 2 H D + 2 Hkv D written per token.  A CTA owns one page of one key or
+// value head, so that the page's maximum never leaves it: the run's values stay in registers between the maximum and
+// the rounding (computed a second time instead, they spilled: 35.9 us against 18.5 for 37 runs of up to 300 tokens).
+// The query heads need no maximum: other CTAs take a token and 16 channels a thread, and up to five heads with the
+// same sines and cosines, all of their loads in flight at once.
 //
-// Angles: position times frequency is a fixed-point product modulo one turn.  The frequency is held as turns per position in
-// units of 2^-64, so the product's low 64 bits are the fraction of a turn, whose upper 32 bits (2^-32 of a turn) are
-// kept: no position loses bits, and no double is needed.  Sine and cosine are the hardware's (absolute error 2^-21 on
-// [-pi, pi]), far below the roundings to bf16 (2^-9) and e4m3 (2^-4) that follow.
+// Angles: position times frequency is a fixed-point product modulo one turn.  The frequency is held as turns per
+// position in units of 2^-64, so the product's low 64 bits are the fraction of a turn, whose upper 32 bits (2^-32 of a
+// turn) are kept: no position loses bits, and no double is needed.  Sine and cosine are the hardware's (absolute error
+// 2^-21 on [-pi, pi]), far below the roundings to bf16 (2^-9) and e4m3 (2^-4) that follow.
 //
-// Measured (8 prompts of up to 4096 tokens, 10 heads of 256): see the figures at the launch.
+// Measured: 8 prompts of up to 4096 tokens, 10 heads of 256: 36.9 us with the launch, 4.5 TB/s; the rest is the two
+// CTAs of 256 threads an SM that the values in registers leave.
 #include "paged.cuh"
 
 namespace rglru {
@@ -77,7 +78,8 @@ __global__ void __launch_bounds__(T) rglru_paged_append_kernel(const __grid_cons
 {
     constexpr int kCols = D / 16, kRows = T / kCols, kHalf = D / 2;
     __shared__ float part[T / 32];
-    __shared__ uint64_t turns[kHalf];  // read by lanes at different places, which the parameter bank would serve one by one
+    // read by lanes at different places, which the parameters' constant bank would serve one by one (43 us, here 37)
+    __shared__ uint64_t turns[kHalf];
     const Batch &b = p.b;
     const int tid = threadIdx.x, role = blockIdx.z;
     const paged::Seq s = paged::load_seq(b, blockIdx.y);
@@ -218,8 +220,8 @@ rglru_status launch(const AppendArgs &p, int rows, cudaStream_t stream)
     rglru_paged_append_kernel<D, NP, T><<<grid, T, 0, stream>>>(p);
     return cuda_status(cudaGetLastError());
 }
-// The smallest CTA that holds a page's share of the longest run: single tokens take 64 threads (256 of them with room for
-// a whole page of 64 slots, 120 registers, left two CTAs an SM: 18 us for 256 sequences against SINGLE_US).
+// The smallest CTA that holds a page's share of the longest run: single tokens take 64 threads (with 256, and room for a
+// whole page of 64 slots in 120 registers, two CTAs fit an SM and 256 sequences took 18 us with the launch, now 14).
 template <int D>
 rglru_status launch(const AppendArgs &p, cudaStream_t stream)
 {

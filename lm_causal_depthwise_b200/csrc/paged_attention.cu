@@ -2,8 +2,9 @@
 //
 //   out[t, h] = sum_p softmax_p(scale * q[t, h] . k[p]) v[p],   pos_t - window < p <= pos_t
 //
-// with k[p], v[p] = code * scale of p's page and head.  Positions outside a row's range
-// are never read or never weighted; a row without any key gives zeros.
+// with k[p], v[p] = code * scale of p's page and head.  Positions outside a row's range are never read or never
+// weighted; a row without any key gives zeros.  One pass over the keys with the softmax's running maximum and sum.
+// Short runs take 16 rows at a time (mma.sync, bound by the cache's bytes), chunks 128 (tcgen05).
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -141,18 +142,21 @@ __device__ __forceinline__ long long piece_begin(long long total, int c, int n) 
 __device__ __forceinline__ int piece_of(long long total, long long t, int n) { return (int)(((t + 1) * n - 1) / total); }
 
 // ------------------------------------------------------------------------------------------------ the kernel
-// One producer warp and four consumer warps.  The producer walks the piece's tiles, looks pages and scales up for eight tiles at
-// a time, and fetches the codes by TMA (128-byte swizzle) into a ring of slots, in the order of their use: k of tile 0, then k of
-// tile t + 1 and v of tile t.  S = Q K^T: consumer warp w has the 16 keys of group w
-// (one page, so one scale) and all 16 rows; the row maxima meet in shared memory, P goes
-// there as f16 in the layout of an mma operand, and O += P V: warp w has channels w D/4 .. of all keys, so that O is never summed
-// across warps.  S of tile t + 1 is computed next to the softmax of tile t: one tile's chain (two barriers,
-// 16 dependent mma, exponentials) is latency, and the next one's products fill it.
-// Codes turn into f16 operands exactly, in registers (the e4m3 form of this mma is no faster: it runs
-// as conversions and f16 products, 5.0 cycles against 2.0).  k's scale multiplies the scores; v's enters the
-// exponent: P holds 2^(s - m + log2 vs - mv) with mv the running maximum of s - m + log2 vs, beside the softmax's own
-// maximum m and sum l = sum 2^(s - m), so that P keeps f16's bits whatever the pages' scales (mv is relative to m: a
-// large score would swallow log2 vs).
+// One producer warp and four consumer warps.  The producer walks the piece's tiles, looks pages and scales up for eight
+// tiles at a time, and fetches the codes by TMA (128-byte swizzle) into a ring of slots, in the order of their use: k of
+// tile 0, then k of tile t + 1 and v of tile t.  S = Q K^T: consumer warp w has the 16 keys of group w (one page, so one
+// scale) and all 16 rows; the row maxima meet in shared memory, P goes there as f16 in the layout of an mma operand, and
+// O += P V: warp w has channels w D/4 .. of all keys, so that O is never summed across warps.  S of tile t + 1 is
+// computed next to the softmax of tile t: one tile's chain (two barriers, 16 dependent mma, exponentials) is latency,
+// and the next one's products fill it.
+// Codes turn into f16 operands exactly, in registers (the e4m3 form of this mma is slower: it runs as conversions and
+// f16 products, 5.0 cycles against 2.2).  k's scale multiplies the scores; v's enters the exponent: P holds
+// 2^(s - m + log2 vs - mv) with mv the running maximum of s - m + log2 vs, beside the softmax's own maximum m and sum
+// l = sum 2^(s - m), so that P keeps f16's bits whatever the pages' scales (mv is relative to m: a large score would
+// swallow log2 vs).
+// Measured, 10 heads of 256 to one key head: 256 sequences over 2048 keys 68 us with the launch and the join (4.0 TB/s
+// of codes; a CTA's tile takes 1.7 us also out of L2, which is the consumers' chain, two CTAs an SM); one sequence over
+// 131072 keys 29 us, of which 6 to the first tile's end and 7 the join.
 //
 // Columns of an 8-key mma tile: column n is key n for even n, n ^ 4 for odd n.  With the swizzle (16-byte chunk c of
 // row r sits at c ^ (r & 7)) both the 16-byte reads of k (two rows a phase) and the 8-byte reads of v (four
@@ -662,9 +666,10 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
     if (tid == 0) plans[cta] = plan;
 }
 
-// Joins the parts of the units that were cut, in their order along the line, whichever CTA was done first.  Units of few parts:
-// a warp takes a row.  Units of many parts (a long sequence over many SMs): a CTA takes 64 channels of a row, its
-// warps every eighth part.  Each CTA lists the items from the plans (one scan) and takes every gridDim.x-th.
+// Joins the parts of the units that were cut, in their order along the line, whichever CTA was done first.  Units of few
+// parts: a warp takes a row.  Units of many parts (a long sequence over many SMs): a CTA takes 64 channels of a row, its
+// half warps every 64th part.  Each CTA lists the items from the plans (one scan) and takes every gridDim.x-th.  Latency
+// bound: 6 to 8 us, of which a launch alone is 3.
 constexpr int kFewParts = 24, kJoinThreads = 1024;
 
 // R: rows of a part
@@ -854,17 +859,20 @@ bool encode_pool(CUtensorMap *m, const uint8_t *base, const Batch &b)
 
 // ------------------------------------------------------------------------------------------------ 128 rows at a time
 // Chunks of tokens: products on tcgen05 with M = 128 rows (row = token * G + head in the group), 64 keys a tile.
-//   warps 0-3   softmax, thread = row = TMEM lane; warp 4 fetches pages by TMA as above; warps 5 and 6 issue S = Q K^T (Q
-//   from TMEM) and O += P V (P from TMEM); warps 7-14 turn v's codes into f16 core matrices of 8 keys x 8 channels (its
-//   channels stay contiguous, so nothing is transposed).
-// k's codes are operands as they arrive: the e4m3 product takes q as two e4m3 terms (e4m3.cuh: exact for all but values below
-// 2^-10 of the row's largest) at twice the f16 rate.  With k converted too, a tile moved 192 KB through shared memory
-// and took 2.0 us, its converters the longest wait; P stays f16, since two e4m3 terms of it would lose the keys
-// below 2^-18 of a row's largest, whose sum counts in a long cache.
-// Exponents, scales and their references as in the 16-row kernel, with the references raised only when a row's
-// maximum passes them by 2^8 (P up to 2^8 keeps f16's bits), since moving O means a pass through TMEM.
+//   warps 0-3   softmax, thread = row = TMEM lane; warp 4 fetches pages by TMA as above; warps 5 and 6 issue S = Q K^T
+//   (Q from TMEM) and O += P V (P from TMEM); warps 7-14 turn v's codes into f16 core matrices of 8 keys x 8 channels
+//   (its channels stay contiguous, so nothing is transposed).
+// k's codes are operands as they arrive: the e4m3 product takes q as two e4m3 terms (e4m3.cuh: exact down to 2^-9 of the
+// row's largest value, below that off by at most 2^-17 of it, far less than the largest's own bf16 rounding) at twice
+// the f16 rate.  With k converted too, a tile moved 192 KB through shared memory and took 2.0 us, its converters the
+// longest wait; P stays f16, since two e4m3 terms of it would lose the keys below 2^-18 of a row's largest, whose sum
+// counts in a long cache.
+// Exponents, scales and their references as in the 16-row kernel, with the references raised only when a row's maximum
+// passes them by 2^8 (P up to 2^8 keeps f16's bits), since moving O means a pass through TMEM.
 // A CTA takes whole units, and the last ones (fewer than CTAs) are cut into equal ranges of tiles: at most one part a
 // CTA, joined as above.
+// Measured: five chunks of up to 256 tokens, 10 heads of 256, 2048 keys each: 50 us with the launch and the join, 300
+// TFLOP/s; a tile takes 1.3 us, the softmax's 64 scores a thread and the two products in turn.
 constexpr int kWideThreads = 480;
 constexpr float kRaise = 8.f;
 constexpr int kNanTiles = 128;  // 8 warps' notes of the tiles that some rows of a unit see and others do not: at most 6 of them
