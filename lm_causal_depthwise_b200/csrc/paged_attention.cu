@@ -859,9 +859,10 @@ bool encode_pool(CUtensorMap *m, const uint8_t *base, const Batch &b)
 
 // ------------------------------------------------------------------------------------------------ 128 rows at a time
 // Chunks of tokens: products on tcgen05 with M = 128 rows (row = token * G + head in the group), 64 keys a tile.
-//   warps 0-3   softmax, thread = row = TMEM lane; warp 4 fetches pages by TMA as above; warps 5 and 6 issue S = Q K^T
-//   (Q from TMEM) and O += P V (P from TMEM); warps 7-14 turn v's codes into f16 core matrices of 8 keys x 8 channels
-//   (its channels stay contiguous, so nothing is transposed).
+//   warps 0-3 and 8-11  softmax, thread = row = TMEM lane and half of the tile's keys (and of q's and O's channels); the
+//   two threads of a row trade their maxima, so that both hold the same references; warp 4 fetches pages by TMA as
+//   above; warps 5 and 6 issue S = Q K^T (Q from TMEM) and O += P V (P from TMEM); warps 7 and 12-18 turn v's codes into
+//   f16 core matrices of 8 keys x 8 channels (its channels stay contiguous, so nothing is transposed).
 // k's codes are operands as they arrive: the e4m3 product takes q as two e4m3 terms (e4m3.cuh: exact down to 2^-9 of the
 // row's largest value, below that off by at most 2^-17 of it, far less than the largest's own bf16 rounding) at twice
 // the f16 rate.  With k converted too, a tile moved 192 KB through shared memory and took 2.0 us, its converters the
@@ -873,7 +874,7 @@ bool encode_pool(CUtensorMap *m, const uint8_t *base, const Batch &b)
 // CTA, joined as above.
 // Measured: five chunks of up to 256 tokens, 10 heads of 256, 2048 keys each: 50 us with the launch and the join, 300
 // TFLOP/s; a tile takes 1.3 us, the softmax's 64 scores a thread and the two products in turn.
-constexpr int kWideThreads = 480;
+constexpr int kWideThreads = 608, kSoftmax = 256;
 constexpr float kRaise = 8.f;
 constexpr int kNanTiles = 128;  // 8 warps' notes of the tiles that some rows of a unit see and others do not: at most 6 of them
 
@@ -883,7 +884,7 @@ struct WideCfg {
     static constexpr int kRaw = kKeyTile * D, kF16 = 2 * kRaw, kRawHalf = kKeyTile * 128;
     static constexpr int kOffRawK = 0, kOffRawV = kRing * kRaw, kOffV = 2 * kRing * kRaw;
     static constexpr int kOffStage = kOffV + 2 * kF16;     // per softmax warp: 32 rows x 32 channels of O on their way out
-    static constexpr int kSmem = kOffStage + 4 * 4096 + 1024;
+    static constexpr int kSmem = kOffStage + 8 * 4096 + 1024;
     static_assert(4 * 32 * 2 * D <= 2 * kF16, "the rows of q pass through v's operands' place");
     static constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384, kColP = 448;
 };
@@ -917,6 +918,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     __shared__ long long scan[kWideThreads / 32];
     __shared__ int nan_count, nan_key0[kNanTiles];
     __shared__ Segment seg_s;
+    __shared__ float2 trade[2][2][kWideRows];  // what the two threads of a row give each other
     const Batch &b = p.b;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = b.H / b.Hkv, cta = blockIdx.x, n_ctas = gridDim.x;
     Plan *plans = reinterpret_cast<Plan *>(reinterpret_cast<char *>(b.ws) + kWsHeaderBytes);
@@ -930,9 +932,9 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 mbar_init(k_full + i, 1), mbar_init(k_free + i, 1), mbar_init(rv_full + i, 1), mbar_init(rv_free + i, 8);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(v_full + i, 8), mbar_init(v_free + i, 1);
-                mbar_init(p_full + i, 128), mbar_init(pv_done + i, 1), mbar_init(drain + i, 1);
+                mbar_init(p_full + i, kSoftmax), mbar_init(pv_done + i, 1), mbar_init(drain + i, 1);
             }
-            mbar_init(&q_full, 128), mbar_init(&s_full, 1), mbar_init(&s_free, 128);
+            mbar_init(&q_full, kSoftmax), mbar_init(&s_full, 1), mbar_init(&s_free, kSoftmax);
             mbar_fence_init();
         }
     }
@@ -1058,11 +1060,11 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     if (lane == 0) mbar_arrive(rv_full + slot);
                 }
             }
-        } else if (warp >= 7) {
+        } else if (warp == 7 || warp >= 12) {
             // ------------------------------------------------------------ v's codes to f16 operands
             // a thread: one key, a quarter of its 16-channel chunks; lanes are consecutive keys, so every phase of a
             // read or write touches each bank once
-            const int cw = warp - 7, row = (cw & 1) * 32 + lane, c0 = (cw >> 1) * (D / 64);
+            const int cw = warp == 7 ? 0 : warp - 11, row = (cw & 1) * 32 + lane, c0 = (cw >> 1) * (D / 64);
             for (int t = 0; t < tiles; ++t) {
                 const int i = n + t, raw = i % kRing, slot = i & 1;
                 if (alive) alive = wait(rv_full + raw, (uint32_t)(i / kRing) & 1u, b.ws, 12);
@@ -1147,57 +1149,66 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 __syncwarp();
             }
         } else {
-            // ------------------------------------------------------------ softmax, thread = row
-            const int r = tid;
+            // ------------------------------------------------------------ softmax, two threads a row
+            const int quarter = warp & 3, half = warp >> 3, r = quarter * 32 + lane;
             const bool live = r < seg.rows;
             const int row = seg.row + (live ? r : 0), pos = seg.ctx + row / G;
             // rows behind the unit's see everything: they are not written, and their tiles need no mask
             const int lo = live ? max(0, pos - p.window + 1) : 0, hi = live ? pos : INT_MAX;
-            const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-            uint8_t *stage = smem + C::kOffStage + warp * 4096, *rows_q = smem + C::kOffV + warp * 64 * D;
+            const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+            uint8_t *stage = smem + C::kOffStage + (quarter + 4 * half) * 4096, *rows_q = smem + C::kOffV + quarter * 64 * D;
+            // the other thread's value; two turns of the place, so that one barrier is enough
+            int turn = 0;
+            auto swap = [&](float2 v) {
+                trade[turn][half][r] = v;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                const float2 u = trade[turn][half ^ 1][r];
+                turn ^= 1;
+                return u;
+            };
             float qs;
             {
-                // The row as two e4m3 terms, times a power of two that brings its largest exponent to 2^7.  A warp fetches whole rows
-                // (a thread fetching its own touches 32 lines an instruction: 4 us), which meet their lane in shared memory, 16-byte
-                // piece x of row r at x ^ r: in the place of v's operands, whose converters wait for q.
-                constexpr int kPerRow = D / 8, kRowsAtOnce = 32 / kPerRow;  // 16-byte pieces of a row; rows of an instruction
+                // The row as two e4m3 terms, times a power of two that brings its largest exponent to 2^7.  A warp
+                // fetches 16 whole rows (a thread fetching its own touches 32 lines an instruction: 4 us), which meet
+                // their lane in shared memory, 16-byte piece x of row r at x ^ r: in the place of v's operands, whose
+                // converters wait for q.
+                constexpr int kPerRow = D / 8, kRowsAtOnce = 32 / kPerRow;  // 16-byte pieces; rows of an instruction
                 const int sub = lane / kPerRow, piece = lane % kPerRow;
+                uint4 q[16 / kRowsAtOnce];
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint4 q[16 / kRowsAtOnce];
-#pragma unroll
-                    for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
-                        const int at = part * 16 + k * kRowsAtOnce + sub, gr = seg.row + warp * 32 + at;
-                        q[k] = warp * 32 + at < seg.rows
-                                   ? __ldg(reinterpret_cast<const uint4 *>(
-                                         p.q + ((size_t)(seg.row0 + gr / G) * b.H + seg.head * G + gr % G) * D) + piece)
-                                   : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
-                        const int at = part * 16 + k * kRowsAtOnce + sub;
-                        *reinterpret_cast<uint4 *>(rows_q + at * 2 * D + ((piece ^ (at & (kPerRow - 1))) << 4)) = q[k];
-                    }
+                for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
+                    const int at = half * 16 + k * kRowsAtOnce + sub, gr = seg.row + quarter * 32 + at;
+                    q[k] = quarter * 32 + at < seg.rows
+                               ? __ldg(reinterpret_cast<const uint4 *>(
+                                     p.q + ((size_t)(seg.row0 + gr / G) * b.H + seg.head * G + gr % G) * D) + piece)
+                               : make_uint4(0, 0, 0, 0);
                 }
-                __syncwarp();
-                auto mine_q = [&](int k) {
+#pragma unroll
+                for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
+                    const int at = half * 16 + k * kRowsAtOnce + sub;
+                    *reinterpret_cast<uint4 *>(rows_q + at * 2 * D + ((piece ^ (at & (kPerRow - 1))) << 4)) = q[k];
+                }
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                auto mine_q = [&](int k) {  // of this thread's half of the channels
+                    k += half * (D / 16);
                     return *reinterpret_cast<const uint4 *>(rows_q + lane * 2 * D + ((k ^ (lane & (kPerRow - 1))) << 4));
                 };
                 uint32_t top = 0;
 #pragma unroll 8
-                for (int k = 0; k < D / 8; ++k) {
+                for (int k = 0; k < D / 16; ++k) {
                     const uint4 u = mine_q(k);
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) top = max(top, max((w[x] << 16) & 0x7f800000u, w[x] & 0x7f800000u));
                 }
+                top = max(top, __float_as_uint(swap(make_float2(__uint_as_float(top), 0.f)).x));
                 int e = max(-126, (int)(top >> 23) - 127 - 7);
                 if (top == 0) e = 0;
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
                 qs = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
                 if (top == 0x7f800000u) qs = __uint_as_float(0x7fc00000u);  // as above (the codes saturate)
 #pragma unroll 2
-                for (int g = 0; g < D / 32; ++g) {  // 32 channels: 8 columns of each term
+                for (int g = 0; g < D / 64; ++g) {  // 32 channels: 8 columns of each term
                     uint32_t hi[8], lo_[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -1211,14 +1222,15 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                             hi[2 * k + x] = h0 | (h1 << 16), lo_[2 * k + x] = l0 | (l1 << 16);
                         }
                     }
-                    tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(g * 8), hi);
-                    tmem_st8(tmem + lane_off + C::kColQ + (uint32_t)(D / 4 + g * 8), lo_);
+                    const uint32_t col = (uint32_t)(half * (D / 8) + g * 8);
+                    tmem_st8(tmem + lane_off + C::kColQ + col, hi);
+                    tmem_st8(tmem + lane_off + C::kColQ + D / 4 + col, lo_);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&q_full);
             }
-            float m = -INFINITY, mv = -INFINITY, l = 0.f;
+            float m = -INFINITY, mv = -INFINITY, l = 0.f;  // l: of this thread's keys
 #pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
                 const int i = n + t, pb = i & 1;
@@ -1226,53 +1238,50 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 __syncwarp();
                 tc_fence_after();
                 const Meta &mt = meta[i % kMeta];
-                const int key0 = mt.key0, okm = mt.ok;
-                f2_t v[32];  // pairs of scores
+                const int key0 = mt.key0 + 32 * half, okm = mt.ok >> (2 * half);
+                f2_t v[16];  // pairs of scores
                 {
-                    uint32_t ra[32], rb[32];
-                    tmem_ld32(tmem + lane_off + C::kColS, ra);
-                    tmem_ld32(tmem + lane_off + C::kColS + 32, rb);
+                    uint32_t ra[32];
+                    tmem_ld32(tmem + lane_off + C::kColS + (uint32_t)(32 * half), ra);
                     tmem_wait_ld();
                     tc_fence_before();
                     mbar_arrive(&s_free);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        v[e] = f2_make(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1]));
-                        v[e + 16] = f2_make(__uint_as_float(rb[2 * e]), __uint_as_float(rb[2 * e + 1]));
-                    }
+                    for (int e = 0; e < 16; ++e) v[e] = f2_make(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1]));
                 }
-                float lv[4];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f2_t c = f2_splat(qs * mt.ks[g]);
-                    lv[g] = mt.lv[g];
+                for (int g = 0; g < 2; ++g) {
+                    const f2_t c = f2_splat(qs * mt.ks[2 * half + g]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[8 * g + e] = f2_mul(v[8 * g + e], c);
                 }
-                const bool inside = okm == 15 && key0 >= lo && key0 + kKeyTile - 1 <= hi;
+                const bool inside = (okm & 3) == 3 && key0 >= lo && key0 + 31 <= hi;
                 if (!__all_sync(0xffffffffu, inside)) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         const bool ok = (okm >> (e >> 3)) & 1;
                         const int k = key0 + 2 * e;
                         v[e] = f2_make(!ok || k < lo || k > hi ? -INFINITY : f2_lo(v[e]),
                                        !ok || k + 1 < lo || k + 1 > hi ? -INFINITY : f2_hi(v[e]));
                     }
                 }
-                float gm[4];
+                float gm[2];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < 2; ++g) {
                     gm[g] = fmaxf(f2_lo(v[8 * g]), f2_hi(v[8 * g]));
 #pragma unroll
                     for (int e = 1; e < 8; ++e) gm[g] = fmaxf(gm[g], fmaxf(f2_lo(v[8 * g + e]), f2_hi(v[8 * g + e])));
                 }
-                const float mt_max = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
-                if (mt_max > m + kRaise || (m == -INFINITY && mt_max > m)) {  // a reference of its own for l; mv is relative to it
+                const float2 og = swap(make_float2(gm[0], gm[1]));
+                const float mt_max = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(og.x, og.y));
+                if (mt_max > m + kRaise || (m == -INFINITY && mt_max > m)) {  // l's own reference; mv is relative to it
                     if (m != -INFINITY) l *= ex2_approx(m - mt_max), mv += m - mt_max;
                     m = mt_max;
                 }
                 const float mz = finite_or_0(m);
-                const float top = fmaxf(fmaxf(gm[0] - mz + lv[0], gm[1] - mz + lv[1]), fmaxf(gm[2] - mz + lv[2], gm[3] - mz + lv[3]));
+                const float lv[2] = {mt.lv[2 * half], mt.lv[2 * half + 1]};
+                const float top = fmaxf(fmaxf(gm[0] - mz + lv[0], gm[1] - mz + lv[1]),
+                                        fmaxf(og.x - mz + mt.lv[2 - 2 * half], og.y - mz + mt.lv[3 - 2 * half]));
                 float f = 1.f;
                 bool move = false;
                 if (top > mv + kRaise || (mv == -INFINITY && top > mv)) {
@@ -1281,12 +1290,13 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     mv = top;
                 }
                 if (__any_sync(0xffffffffu, move)) {
-                    // O holds the tiles before: wait for the last of them, then scale in place (a row moves after its first tile)
+                    // O holds the tiles before: wait for the last of them, then scale in place, half of the channels a
+                    // thread (a row moves after its first tile)
                     if (alive) alive = wait(pv_done + ((i - 1) & 1), (uint32_t)((i - 1) / 2) & 1u, b.ws, 22);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
+                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                         uint32_t o[32];
                         tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)c, o);
                         tmem_wait_ld();
@@ -1297,11 +1307,11 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                uint32_t pk[32];
-                f2_t l2[2] = {f2_splat(0.f), f2_splat(0.f)};
+                uint32_t pk[2][8];
+                f2_t l2[2];
                 const float vz = finite_or_0(mv);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < 2; ++g) {
                     // P = 2^(s - m + d), l sums 2^(s - m).  Where d is above 100 (values 2^100 apart), 2^(s - m) would
                     // underflow under a P that counts: then the exponential is taken at s - m + d - 100, at most 2^-92.
                     const float d = lv[g] - vz, over = fmaxf(0.f, d - 100.f);
@@ -1313,9 +1323,9 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                         const f2_t q = f2_make(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
                         lg[e & 1] = e < 2 ? q : f2_add(lg[e & 1], q);
                         const f2_t y = f2_mul(q, w);
-                        pk[8 * g + e] = pack_f16(f2_lo(y), f2_hi(y));
+                        pk[g][e] = pack_f16(f2_lo(y), f2_hi(y));
                     }
-                    l2[g & 1] = f2_fma(f2_add(lg[0], lg[1]), f2_splat(ex2_approx(-over)), l2[g & 1]);
+                    l2[g] = f2_mul(f2_add(lg[0], lg[1]), f2_splat(ex2_approx(-over)));
                 }
                 l2[0] = f2_add(l2[0], l2[1]);
                 l += f2_lo(l2[0]) + f2_hi(l2[0]);
@@ -1323,7 +1333,9 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 if (i >= 2 && alive) alive = wait(pv_done + pb, (uint32_t)(i / 2 - 1) & 1u, b.ws, 23);
                 __syncwarp();
                 tc_fence_after();
-                tmem_st32(tmem + lane_off + C::kColP + (uint32_t)(pb * 32), pk);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    tmem_st8(tmem + lane_off + C::kColP + (uint32_t)(pb * 32 + half * 16 + g * 8), pk[g]);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full + pb);
@@ -1332,13 +1344,16 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             if (alive) alive = wait(pv_done + (last & 1), (uint32_t)(last / 2) & 1u, b.ws, 24);
             __syncwarp();
             tc_fence_after();
+            const float2 other = swap(make_float2(l, alive ? 1.f : 0.f));
+            l = half == 0 ? l + other.x : other.x + l;
+            alive = alive && other.y != 0.f;
             const int bad = min(nan_count, kNanTiles);
             const bool is_whole = seg.parts == 1;
             float *slot = parts + (size_t)cta * part_floats(kWideRows, D);
             const float o_scale = l == 0.f ? 0.f : ex2_approx(finite_or_0(mv)) / l;
-            if (!is_whole && live && alive) *reinterpret_cast<float4 *>(slot + 4 * r) = make_float4(m, mv, l, 0.f);
+            if (!is_whole && live && alive && half == 0) *reinterpret_cast<float4 *>(slot + 4 * r) = make_float4(m, mv, l, 0.f);
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 uint32_t o[32];
                 tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)c, o);
                 tmem_wait_ld();
@@ -1365,12 +1380,13 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {  // four rows at a time, eight lanes each
-                    const int rr = 4 * k + (lane >> 3), x = lane & 7, at = warp * 32 + rr;
+                    const int rr = 4 * k + (lane >> 3), x = lane & 7, at = quarter * 32 + rr;
                     const uint4 w = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((x ^ (rr & 7)) << 4));
                     if (at < seg.rows && alive) {
                         if (is_whole) {
                             const int gr = seg.row + at;
-                            *reinterpret_cast<uint2 *>(p.out + ((size_t)(seg.row0 + gr / G) * b.H + seg.head * G + gr % G) * D + c + 4 * x) =
+                            *reinterpret_cast<uint2 *>(
+                                p.out + ((size_t)(seg.row0 + gr / G) * b.H + seg.head * G + gr % G) * D + c + 4 * x) =
                                 make_uint2(pack_bf16(__uint_as_float(w.x), __uint_as_float(w.y)),
                                            pack_bf16(__uint_as_float(w.z), __uint_as_float(w.w)));
                         } else {
@@ -1379,7 +1395,8 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     }
                 }
             }
-            if (tid == 0 && !is_whole && seg.part == 0) plans[cta] = {(short)seg.parts, (short)seg.rows, seg.row0, seg.row, seg.head};
+            if (tid == 0 && !is_whole && seg.part == 0)
+                plans[cta] = {(short)seg.parts, (short)seg.rows, seg.row0, seg.row, seg.head};
             tc_fence_before();
         }
         n += tiles;
