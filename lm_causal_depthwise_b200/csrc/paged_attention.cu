@@ -29,7 +29,7 @@ struct AttendArgs {
 // A unit is 16 rows (row = token * G + head in the group, G = H / Hkv) of one sequence and key/value head;
 // its work is the 64-key tiles of the sequence's attended range.  All units' tiles form one line, cut into
 // gridDim.x equal pieces: long and short sequences balance, and one long sequence spreads over every SM.
-constexpr int kRowTile = 16, kKeyTile = 64, kMinTiles = 2;
+constexpr int kRowTile = 16, kKeyTile = 64, kMinTiles = 2, kManyTiles = 10;
 constexpr int kConsumers = 128, kThreads = kConsumers + 32;
 constexpr int kSms = 148, kMaxCtas = 3 * kSms;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -46,10 +46,12 @@ struct Meta {                // of one tile in the ring, written by the producer
 
 template <int D>
 struct Cfg {
-    static constexpr int kCtasPerSm = D == 256 ? 2 : 3;
+    // three CTAs with few slots rather than two with more: a tile's chain is latency (256 sequences over 2048 keys, D 256:
+    // 62 us against 67; two CTAs with three slots take 67 as well)
+    static constexpr int kCtasPerSm = 3;
     static constexpr int kHalf = kKeyTile * 128;      // 64 keys x 128 channels (one swizzled box column)
     static constexpr int kSlotBytes = kKeyTile * D;   // k or v of a tile
-    static constexpr int kSlots = D == 256 ? 5 : 7;
+    static constexpr int kSlots = D == 256 ? 3 : 7;
     static constexpr int kQBytes = kRowTile * D * 2;  // a unit's rows as they come, and as f16 operands
     static constexpr int kSmem = kSlots * kSlotBytes + 2 * kQBytes + 1024;
 };
@@ -66,7 +68,7 @@ constexpr size_t kPlanBytes = (size_t)kMaxCtas * sizeof(Plan);
 __host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size_t)rows * (4 + D); }
 inline size_t attention_bytes(int D)
 {
-    const size_t few = (size_t)(D == 256 ? 2 : 3) * kSms * 2 * part_floats(kRowTile, D), wide = kSms * part_floats(kWideRows, D);
+    const size_t few = (size_t)kMaxCtas * 2 * part_floats(kRowTile, D), wide = kSms * part_floats(kWideRows, D);
     return kWsHeaderBytes + align_up_d(kPlanBytes, 256) + (few > wide ? few : wide) * 4;
 }
 
@@ -154,9 +156,9 @@ __device__ __forceinline__ int piece_of(long long total, long long t, int n) { r
 // 2^(s - m + log2 vs - mv) with mv the running maximum of s - m + log2 vs, beside the softmax's own maximum m and sum
 // l = sum 2^(s - m), so that P keeps f16's bits whatever the pages' scales (mv is relative to m: a large score would
 // swallow log2 vs).
-// Measured, 10 heads of 256 to one key head: 256 sequences over 2048 keys 68 us with the launch and the join (4.0 TB/s
-// of codes; a CTA's tile takes 1.7 us also out of L2, which is the consumers' chain, two CTAs an SM); one sequence over
-// 131072 keys 29 us, of which 6 to the first tile's end and 7 the join.
+// Measured, 10 heads of 256 to one key head: 256 sequences over 2048 keys 65 us with the launch and the join (4.1 TB/s
+// of codes; a CTA's tile takes 1.7 us and more also out of L2, which is the consumers' chain); one sequence over 131072
+// keys 29 us, of which 6 to the first tile's end and 7 the join.
 //
 // Columns of an 8-key mma tile: column n is key n for even n, n ^ 4 for odd n.  With the swizzle (16-byte chunk c of
 // row r sits at c ^ (r & 7)) both the 16-byte reads of k (two rows a phase) and the 8-byte reads of v (four
@@ -1443,7 +1445,11 @@ rglru_status launch(const AttendArgs &p, cudaStream_t stream)
     if ((int64_t)p.b.max_new * (p.b.H / p.b.Hkv) <= 2 * kRowTile) {
         const rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_kernel<D>), C::kSmem, flag);
         if (st != RGLRU_OK) return st;
-        const int grid = kSms * C::kCtasPerSm;
+        // A third CTA an SM pays when there is much to do (the figures at Cfg); with little, more pieces are more to join
+        // (one sequence over 131072 keys, 2048 tiles: 444 pieces 30.6 us, 296 28.8).
+        const int reach = p.window < p.b.max_total - p.b.max_new ? p.window + p.b.max_new : p.b.max_total;
+        const int64_t tiles = (int64_t)p.b.S * p.b.Hkv * (reach / kKeyTile + 1);
+        const int grid = kSms * (tiles < kManyTiles * kSms * C::kCtasPerSm ? 2 : C::kCtasPerSm);
         rglru_paged_attention_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p, tm_k, tm_v);
         if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
         return launch_join<D, kRowTile>(p, grid, stream);
