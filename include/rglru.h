@@ -634,6 +634,80 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
                                              const float *k_scale, const void *v_cache, const float *v_scale, void *out,
                                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * The five serving calls with their parameters in a block, for callers to whom
+ * each argument of a foreign call costs (an interpreter: a step makes these
+ * calls for every token).  args points to the struct of the call, its members
+ * the call's parameters in their order; the result is the call's.
+ */
+typedef enum {
+    RGLRU_CALL_ADD_RMSNORM = 0,
+    RGLRU_CALL_ADD_RMSNORM_E4M3 = 1,
+    RGLRU_CALL_LINEAR_W4 = 2,
+    RGLRU_CALL_PAGED_APPEND = 3,
+    RGLRU_CALL_PAGED_ATTENTION = 4
+} rglru_call;
+
+typedef struct {
+    int M, N;
+    const void *x, *residual;
+    const float *weight;
+    float eps;
+    void *residual_out, *out;
+    cudaStream_t stream;
+} rglru_add_rmsnorm_args;
+
+typedef struct {
+    int M, N, group;
+    const void *x, *residual;
+    const float *weight;
+    float eps;
+    void *residual_out, *out;
+    float *out_scale;
+    cudaStream_t stream;
+} rglru_add_rmsnorm_e4m3_args;
+
+typedef struct {
+    int M, N, K, group;
+    const void *A;
+    const float *A_scale;
+    int a_group;
+    const void *W, *W_scale;
+    const float *bias;
+    void *out;
+    cudaStream_t stream;
+} rglru_linear_w4_args;
+
+typedef struct {
+    int rows, S, H, Hkv, head_dim, page_size, num_pages, max_pages, max_new, max_total;
+    const void *qkv;
+    const int32_t *cu_tokens, *ctx_len, *block_table;
+    float rope_base;
+    void *q_out, *k_cache;
+    float *k_scale;
+    void *v_cache;
+    float *v_scale;
+    void *workspace;
+    size_t workspace_bytes;
+    cudaStream_t stream;
+} rglru_paged_append_args;
+
+typedef struct {
+    int rows, S, H, Hkv, head_dim, page_size, num_pages, max_pages, max_new, max_total, window;
+    float scale;
+    const void *q;
+    const int32_t *cu_tokens, *ctx_len, *block_table;
+    const void *k_cache;
+    const float *k_scale;
+    const void *v_cache;
+    const float *v_scale;
+    void *out, *workspace;
+    size_t workspace_bytes;
+    cudaStream_t stream;
+} rglru_paged_attention_args;
+
+RGLRU_API rglru_status rglru_serving_call(rglru_call call, const void *args);
+
 #ifdef __cplusplus
 }
 #endif

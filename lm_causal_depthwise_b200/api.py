@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -32,7 +33,7 @@ SYMBOLS = ("rglru_version", "rglru_status_string", "rglru_workspace_size", "rglr
            "rglru_mqa_block_prefill", "rglru_mqa_decode_workspace_size", "rglru_mqa_decode_step",
            "rglru_mqa_residual_block_workspace_size", "rglru_mqa_residual_block_prefill", "rglru_carry_scan",
            "rglru_add_rmsnorm", "rglru_add_rmsnorm_e4m3", "rglru_linear_w4", "rglru_paged_append",
-           "rglru_paged_attention_workspace_size", "rglru_paged_attention")
+           "rglru_paged_attention_workspace_size", "rglru_paged_attention", "rglru_serving_call")
 
 _lib = None
 
@@ -132,6 +133,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rglru_paged_attention_workspace_size.argtypes = [i, i, i]
     lib.rglru_paged_attention.restype = i
     lib.rglru_paged_attention.argtypes = [i] * 11 + [f] + [vp] * 10 + [sz, vp]
+    lib.rglru_serving_call.restype = i
+    lib.rglru_serving_call.argtypes = [i, ctypes.c_char_p]
     _lib = lib
     return lib
 
@@ -860,30 +863,41 @@ E4M3 = torch.float8_e4m3fn
 FULL_WINDOW = 1 << 30  # a window that reaches every position
 
 
+_Tensor = torch.Tensor
+
+
 def _need(t, name: str, shape: tuple, dtype, dev) -> None:
     """_check for calls that are made for every token: one expression when all is well, the
     message from _check otherwise."""
-    if not (type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.device == dev
+    if not (type(t) is _Tensor and t.shape == shape and t.dtype is dtype and t.device == dev
             and t.is_contiguous()):
         _check(t, name, shape, dtype, dev)
 
 
+# The serving calls' parameters as their structs in the header (rglru_serving_call), stream last.
+_CALLS = {name: (k, struct.Struct(f"@{members}").pack) for k, (name, members) in enumerate((
+    ("rglru_add_rmsnorm", "2i3Pf3P"), ("rglru_add_rmsnorm_e4m3", "3i3Pf4P"), ("rglru_linear_w4", "4i2Pi5P"),
+    ("rglru_paged_append", "10i4Pf6PNP"), ("rglru_paged_attention", "11if10PNP")))}
+
+
 def _enqueue(name: str, dev: torch.device, *args) -> None:
-    """Runs the library call ``name`` on ``dev`` (made current for the launch) and its current stream."""
+    """Runs the serving call ``name`` on ``dev`` (made current for the launch) and its current stream."""
     if dev.type != "cuda":
         raise ValueError(f"the tensors must be CUDA tensors, got device {dev}")
-    fn = getattr(_lib or load(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    call, pack = _CALLS[name]
+    index = dev.index
+    block = pack(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == torch._C._cuda_getDevice():
+        st = (_lib or load()).rglru_serving_call(call, block)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            st = (_lib or load()).rglru_serving_call(call, block)
     if st != OK:
         raise RGLRUError(st, name)
 
 
 def _addr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _norm_args(x, residual, weight, residual_out):
@@ -897,7 +911,8 @@ def _norm_args(x, residual, weight, residual_out):
         _need(residual, "residual", x.shape, torch.bfloat16, dev)
         if residual_out is None:
             residual_out = torch.empty_like(x)
-        _need(residual_out, "residual_out", x.shape, torch.bfloat16, dev)
+        else:
+            _need(residual_out, "residual_out", x.shape, torch.bfloat16, dev)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     return x.numel() // N, N, dev, residual_out
@@ -909,7 +924,8 @@ def add_rmsnorm(x, residual, weight, eps: float = 1e-6, out=None, residual_out=N
     M, N, dev, residual_out = _norm_args(x, residual, weight, residual_out)
     if out is None:
         out = torch.empty_like(x)
-    _need(out, "out", x.shape, torch.bfloat16, dev)
+    else:
+        _need(out, "out", x.shape, torch.bfloat16, dev)
     _enqueue("rglru_add_rmsnorm", dev, M, N, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
              _addr(residual_out), out.data_ptr())
     return out, (x if residual is None else residual_out)
@@ -924,11 +940,13 @@ def add_rmsnorm_e4m3(x, residual, weight, eps: float = 1e-6, group: int = 128, o
         raise ValueError(f"N = {N} is not a multiple of group = {group}")
     if out is None:
         out = torch.empty(x.shape, dtype=E4M3, device=dev)
-    _need(out, "out", x.shape, E4M3, dev)
+    else:
+        _need(out, "out", x.shape, E4M3, dev)
     shape = (*x.shape[:-1], N // group)
     if scale is None:
         scale = torch.empty(shape, dtype=torch.float32, device=dev)
-    _need(scale, "scale", shape, torch.float32, dev)
+    else:
+        _need(scale, "scale", shape, torch.float32, dev)
     _enqueue("rglru_add_rmsnorm_e4m3", dev, M, N, group, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
              _addr(residual_out), out.data_ptr(), scale.data_ptr())
     return out, scale, (x if residual is None else residual_out)
@@ -960,7 +978,8 @@ def linear_w4(A, W, W_scale, bias=None, A_scale=None, out=None) -> torch.Tensor:
         _need(bias, "bias", (N,), torch.float32, dev)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", (M, N), torch.bfloat16, dev)
+    else:
+        _need(out, "out", (M, N), torch.bfloat16, dev)
     _enqueue("rglru_linear_w4", dev, M, N, K, K // G, A.data_ptr(), _addr(A_scale), a_group, W.data_ptr(),
              W_scale.data_ptr(), _addr(bias), out.data_ptr())
     return out
@@ -1036,7 +1055,8 @@ def paged_append(qkv, batch: PagedBatch, cache: PagedCache, rope_base: float = 1
     _need(qkv, "qkv", (rows, (H + 2 * Hkv) * D), torch.bfloat16, dev)
     if q_out is None:
         q_out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
-    _need(q_out, "q_out", (rows, H * D), torch.bfloat16, dev)
+    else:
+        _need(q_out, "q_out", (rows, H * D), torch.bfloat16, dev)
     workspace, nb = _paged_workspace(workspace, 4096, dev)
     _enqueue("rglru_paged_append", dev, rows, S, H, Hkv, D, ps, P, max_pages, batch.max_new, batch.max_total,
              qkv.data_ptr(), batch.cu_tokens.data_ptr(), batch.ctx_len.data_ptr(), batch.block_table.data_ptr(),
@@ -1066,7 +1086,8 @@ def paged_attention(q, batch: PagedBatch, cache: PagedCache, window: int = MQA_W
     _need(q, "q", (rows, H * D), torch.bfloat16, dev)
     if out is None:
         out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", (rows, H * D), torch.bfloat16, dev)
+    else:
+        _need(out, "out", (rows, H * D), torch.bfloat16, dev)
     if workspace is None:
         workspace = new_workspace(paged_attention_workspace_size(H, Hkv, D), dev)
     workspace, nb = _paged_workspace(workspace, 0, dev)

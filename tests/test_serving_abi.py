@@ -158,3 +158,43 @@ def test_binding_refuses(lib):
         api.paged_attention(qkv[:, :500].contiguous(), _batch(), cache)
     with pytest.raises(api.RGLRUError):
         api.paged_attention_workspace_size(4, 3, 128)
+
+
+def test_the_block_form_reaches_the_same_checks(lib):
+    """rglru_serving_call: each parameter arrives in its place (its own refusal), unknown calls and no block are refused."""
+    call = lib.rglru_serving_call
+    assert call(5, b"\0" * 256) == call(-1, b"\0" * 256) == call(0, None) == api.ERR_INVALID_ARG
+
+    def tries(name, good, cases):
+        k, pack = api._CALLS[name]
+        assert call(k, pack(*good.values())) == good_status
+        for key, value, st in cases:
+            assert key in good
+            assert call(k, pack(*{**good, key: value}.values())) == st, (name, key)
+
+    # a size of zero first: nothing is launched, and every later refusal of its own status shows its place
+    good_status = api.ERR_UNSUPPORTED
+    norm = dict(M=4, N=12, x=MB, r=2 * MB, w=3 * MB, eps=1e-6, ro=4 * MB, out=5 * MB, stream=0)
+    tries("rglru_add_rmsnorm", norm, [("M", 0, 1), ("eps", 0.0, 1), ("N", 0, 1)])
+    norm8 = dict(M=4, N=512, group=48, x=MB, r=2 * MB, w=3 * MB, eps=1e-6, ro=4 * MB, out=5 * MB, sc=6 * MB, stream=0)
+    tries("rglru_add_rmsnorm_e4m3", norm8, [("M", 0, 1), ("eps", -1.0, 1)])
+    w4 = dict(M=65, N=100, K=256, group=64, A=MB, As=0, ag=0, W=2 * MB, Ws=3 * MB, b=4 * MB, out=5 * MB, stream=0)
+    tries("rglru_linear_w4", w4, [("N", 0, 1), ("K", 0, 1)])
+    at = {n: 16 * MB * (i + 1) for i, n in enumerate(NAMES)}
+    sizes = dict(rows=8, S=2, H=4, Hkv=2, D=128, page=16, pages=8, max_pages=4, max_new=4, max_total=64)
+    good_status = api.ERR_WORKSPACE
+    append = dict(**sizes, **{n: at[n] for n in ("qkv", "cu", "ctx", "table")}, base=10000.0,
+                  **{n: at[n] for n in ("q", "k", "ks", "v", "vs", "ws")}, wsb=16, stream=0)
+    bad = [("rows", 0, 1), ("D", 64, 2), ("page", 24, 2), ("max_total", 65, 1), ("cu", 8, 1), ("table", 0, 1), ("vs", 8, 1),
+           ("k", 8, 1), ("ws", 0, 3)]
+    tries("rglru_paged_append", append, bad + [("wsb", 15, 3)])
+    attend = dict(**sizes, window=32, scale=0.1, **{n: at[n] for n in ("qkv", "cu", "ctx", "table", "k", "ks", "v", "vs")},
+                  out=at["q"], ws=at["ws"], wsb=16, stream=0)
+    tries("rglru_paged_attention", attend, bad)
+    good_status = api.ERR_INVALID_ARG
+    room = dict(wsb=1 << 26)
+    tries("rglru_paged_append", {**append, **room, "base": 1.0}, [("wsb", 16, 3)])
+    tries("rglru_paged_append", {**append, **room, "q": 8}, [("wsb", 16, 3)])
+    tries("rglru_paged_attention", {**attend, **room, "window": 0}, [("wsb", 16, 3)])
+    tries("rglru_paged_attention", {**attend, **room, "scale": 0.0}, [("wsb", 16, 3)])
+    tries("rglru_paged_attention", {**attend, **room, "out": at["v"]}, [("wsb", 16, 3)])
