@@ -8,7 +8,7 @@
 // kernel the sum is read from registers instead of from memory: 8 bytes per element with a bf16 output (7 with an 8-bit
 // one) against 10 for an addition and rglru_rmsnorm.  h is rounded to bf16 before the norm, so that the result is what
 // the two calls give.  The sum of squares, the mean and the scaled row are fp32.  Memory bound: 32768 x 2560 takes
-// 106 us, 6.3 TB/s; a few rows take the launch (4 x 2560: 10 us).
+// 106 us, 6.3 TB/s; a few rows take the launch (4 x 2560: 9 us, 4 on the device).
 #include "e4m3.cuh"
 #include "internal.h"
 

@@ -221,7 +221,7 @@ rglru_status launch(const AppendArgs &p, int rows, cudaStream_t stream)
     return cuda_status(cudaGetLastError());
 }
 // The smallest CTA that holds a page's share of the longest run: single tokens take 64 threads (with 256, and room for a
-// whole page of 64 slots in 120 registers, two CTAs fit an SM and 256 sequences took 18 us with the launch, now 14).
+// whole page of 64 slots in 120 registers, two CTAs fit an SM and 256 sequences took 18 us with the launch, with 64 threads 14).
 template <int D>
 rglru_status launch(const AppendArgs &p, cudaStream_t stream)
 {
