@@ -595,7 +595,7 @@ RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group, const voi
  * larger of the scale it had and that of the new tokens; when it grew, the
  * slots before the first new one are rounded again at the new scale.  Slots
  * behind the last new token are left as they were.  Every page that the call
- * writes must be written for one sequence only.  The workspace (at least
+ * writes must be written for one sequence, and stand once in its table.  The workspace (at least
  * rglru_linear_workspace_size() bytes, zero-filled once) holds the status word.
  */
 RGLRU_API rglru_status rglru_paged_append(

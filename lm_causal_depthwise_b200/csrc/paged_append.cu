@@ -17,8 +17,8 @@
 // turn) are kept: no position loses bits, and no double is needed.  Sine and cosine are the hardware's (absolute error
 // 2^-21 on [-pi, pi]), far below the roundings to bf16 (2^-9) and e4m3 (2^-4) that follow.
 //
-// Measured: 8 prompts of up to 4096 tokens, 10 heads of 256: 36.9 us with the launch, 4.5 TB/s; the rest is the two
-// CTAs of 256 threads an SM that the values in registers leave.
+// Measured: 8 prompts of up to 4096 tokens, 10 heads of 256: 35.1 us with the launch, 4.8 TB/s; 37 runs of up to 300
+// tokens, 16 heads of 128 on 4, pages of 16: 18.5 us.
 #include "paged.cuh"
 
 namespace rglru {
@@ -71,10 +71,12 @@ __device__ __forceinline__ void rotate(float (&x1)[8], float (&x2)[8], const flo
 
 constexpr int kQHeads = 5;  // query heads of a CTA, at most
 
+// 512 threads are held to 64 registers, so that two such CTAs fit an SM (twice the loads in flight of two CTAs of 256
+// threads with four passes, which took 36.9 us for the prompts above).
 // D channels a head, NP passes of T / (D / 16) rows of the run; a thread holds the channels
 // c .. c + 7 and c + D/2 .. c + D/2 + 7 of a row.
 template <int D, int NP, int T>
-__global__ void __launch_bounds__(T) rglru_paged_append_kernel(const __grid_constant__ AppendArgs p)
+__global__ void __launch_bounds__(T, T == 512 ? 2 : 0) rglru_paged_append_kernel(const __grid_constant__ AppendArgs p)
 {
     constexpr int kCols = D / 16, kRows = T / kCols, kHalf = D / 2;
     __shared__ float part[T / 32];
@@ -230,7 +232,7 @@ rglru_status launch(const AppendArgs &p, cudaStream_t stream)
     if (items <= 128) return launch<D, 2, 64>(p, rows, stream);
     if (items <= 256) return launch<D, 2, 128>(p, rows, stream);
     if (items <= 512) return launch<D, 2, 256>(p, rows, stream);
-    if (items <= 1024) return launch<D, 4, 256>(p, rows, stream);
+    if (items <= 1024) return launch<D, 2, 512>(p, rows, stream);
     return launch<D, 8, 256>(p, rows, stream);
 }
 
