@@ -221,8 +221,10 @@ RGLRU_API rglru_status rglru_get_device_status(void *workspace, cudaStream_t str
  * RGLRU_ERR_TIMEOUT instead of hanging; on a decode workspace, CTA `unit` of
  * the next rglru_decode_step calls keeps its half of the gate GEMM's operand
  * from its peer CTA, whose wait runs out the same way (the call then takes a
- * few seconds).  unit = -1 turns it off.  The flag lives in the workspace
- * header and is enqueued on `stream`.
+ * few seconds); on an attention workspace, CTA `unit` of the next
+ * rglru_paged_attention calls keeps back its first tile of values.  unit = -1
+ * turns it off.  The flag lives in the workspace header and is enqueued on
+ * `stream`.
  */
 RGLRU_API rglru_status rglru_debug_suppress_publish(void *workspace, int unit, cudaStream_t stream);
 

@@ -61,7 +61,7 @@ struct Plan {  // the unit that begins in a CTA's piece and does not end there: 
     short parts, rows;
     int row0, row, head;  // the sequence's first row; the unit's first (token * G + head in group), its key/value head
 };
-// Workspace: header, plans, then partial results, R rows each: m, mv, l, pad (float4) and O [R][D].  The 16-row
+// Workspace: header, plans, then partial results, R rows each: m, mv, l, lost (float4) and O [R][D].  The 16-row
 // kernel has two a CTA (slot 2 c: a unit begun in an earlier CTA; 2 c + 1: one begun here), the 128-row kernel one.
 constexpr int kWideRows = 128;
 constexpr size_t kPlanBytes = (size_t)kMaxCtas * sizeof(Plan);
@@ -89,22 +89,61 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs &p, int i)
 }
 
 // ------------------------------------------------------------------------------------------------ pieces
-// A wait gives up after 2 s, records it and returns false; the caller goes on without waiting again (every loop is bounded),
-// and writes no result.
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, WsHeader *ws, int where)
+// A wait gives up after 2 s, or once another of its CTA has (`lost`, in shared memory); the first to give up records it.
+// Who gave up waits no more and passes the CTA's barriers with the others, but arrives on no mbarrier and starts no copy
+// or product: every arrival stands for a wait that was won, so the others run out of theirs as well, and none takes a slot
+// that is half full for a full one.  The rows held up are not written, and the CTA's parts say that they are not there.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, WsHeader *ws, volatile int *lost, int where)
 {
     const uint64_t t0 = sm100::globaltimer();
-    while (sm100::globaltimer() - t0 < kTimeoutNs)
+    do {
         if (sm100::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+        if (*lost) return false;
+    } while (sm100::globaltimer() - t0 < kTimeoutNs);
+    *lost = 1;
+    __threadfence_block();
     atomicCAS(&ws->status, 0, (int)RGLRU_ERR_TIMEOUT);
     atomicCAS(&ws->detail, 0, (int)(blockIdx.x << 8) | (where + 1));
     return false;
 }
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, WsHeader *ws, int where)
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, WsHeader *ws, volatile int *lost, int where)
 {
-    return sm100::mbar_try_wait(bar, parity) || wait_slow(bar, parity, ws, where);
+    return sm100::mbar_try_wait(bar, parity) || wait_slow(bar, parity, ws, lost, where);
+}
+// For what is in flight when a CTA ends, whether or not a wait was lost.
+__device__ __noinline__ void drain_wait(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = sm100::globaltimer();
+    while (!sm100::mbar_try_wait_sleep(bar, parity, 20000u) && sm100::globaltimer() - t0 < kTimeoutNs) {
+    }
+}
+// Test hook (rglru_debug_suppress_publish): the CTA it names keeps back the arrival on its first tile of v until the
+// waits for it have run out.  (The flag is read long before that: its way from memory would show in every call.)
+__device__ __forceinline__ int hook(const WsHeader *ws)
+{
+    int unit;
+    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(unit) : "l"(&ws->debug_unit_plus1));  // volatile: stays where it is called
+    return unit;
+}
+__device__ __noinline__ void give_back(uint64_t *bar, volatile int *lost)
+{
+    const uint64_t t0 = sm100::globaltimer();
+    while (*lost == 0 && sm100::globaltimer() - t0 < 2 * kTimeoutNs) {
+    }
+    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
+    __syncwarp();
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// barrier `id` of `count` threads; whether any of them has x
+__device__ __forceinline__ bool bar_any(int id, int count, bool x)
+{
+    int any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"((int)x), "r"(id), "r"(count)
+                 : "memory");
+    return any != 0;
+}
 __device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes)
 {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(sm100::smem_u32(bar)), "r"(bytes) : "memory");
@@ -181,7 +220,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
     __shared__ uint4 pbuf[4][32];
     __shared__ float lsum[4][kRowTile];
     __shared__ long long scan[kThreads / 32];
-    __shared__ int where[3];
+    __shared__ int where[3], lost;
     __shared__ Geometry where_g;
     const Batch &b = p.b;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -192,7 +231,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
     if (tid < kSlots) {
         sm100::mbar_init(full + tid, 1);
         sm100::mbar_init(empty + tid, kConsumers / 32);
-        if (tid == 0) sm100::mbar_init(&q_full, 1), sm100::mbar_init(&q_empty, kConsumers / 32);
+        if (tid == 0) sm100::mbar_init(&q_full, 1), sm100::mbar_init(&q_empty, kConsumers / 32), lost = 0;
         sm100::mbar_fence_init();
     }
     const int per = (b.S + kThreads - 1) / kThreads, s0 = min(b.S, tid * per), s1 = min(b.S, s0 + per);
@@ -246,13 +285,14 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
 
     if (warp == kConsumers / 32) {
         // ---------------------------------------------------------------- producer
+        const int named = hook(b.ws);
         const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile);
         int seq = where[0], unit = where[1], tile = where[2], it = 0, units = 0, slot = 0, uses = 0;
         Geometry g = where_g;
-        bool alive = true;
-        // a slot to fill: `boxes` of this lane's c1 (lanes 0 .. 3 with `leads`), k or v
+        int held = -1;  // slot whose arrival is kept back
+        // a slot to fill: `boxes` of this lane's c1 (lanes 0 .. 3 with `leads`), k or v; false when the wait for it was lost
         auto fill = [&](const CUtensorMap *tm, bool leads, int c1) {
-            if (uses > 0 && alive) alive = wait(empty + slot, (uint32_t)(uses - 1) & 1u, b.ws, 0);
+            if (uses > 0 && !__all_sync(0xffffffffu, wait(empty + slot, (uint32_t)(uses - 1) & 1u, b.ws, &lost, 0))) return false;
             const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, leads));
             if (lane == 0) mbar_expect(full + slot, n * (uint32_t)box * D);
             __syncwarp();
@@ -261,90 +301,98 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
 #pragma unroll
                 for (int x = 0; x < D / 128; ++x) sm100::tma_load_2d(dst + x * C::kHalf, tm, full + slot, x * 128, c1);
             }
+            return true;
         };
-        auto filled = [&]() {
+        auto filled = [&](bool first_v = false) {
             __syncwarp();
-            if (lane == 0) sm100::mbar_arrive(full + slot);
+            if (first_v && named == cta + 1)
+                held = slot;
+            else if (lane == 0)
+                sm100::mbar_arrive(full + slot);
             if (++slot == kSlots) slot = 0, ++uses;
         };
         bool v_leads = false;  // of the tile whose v comes next
         int v_c1 = 0;
-        for (; it < count; ++units) {
-            const int per_head = g.units / b.Hkv, head = unit / per_head, row = unit % per_head * kRowTile;
-            const int rows = min(kRowTile, g.n * G - row);
-            const int lo = max(0, g.ctx + row / G - p.window + 1), hi = g.ctx + (row + rows - 1) / G + 1;
-            const int tiles = min(g.tiles - tile, count - it);  // of this unit, in this piece
-            // its query rows, once the consumers have turned the last unit's into operands
-            if (units > 0 && alive) alive = wait(&q_empty, (uint32_t)(units - 1) & 1u, b.ws, 3);
-            if (lane == 0) sm100::mbar_arrive_expect_tx(&q_full, (uint32_t)rows * D * 2);
-            __syncwarp();
-            if (lane < rows) {
-                const int r = row + lane;
-                sm100::bulk_load(qbuf + lane * D * 2, p.q + ((size_t)(g.row0 + r / G) * b.H + head * G + r % G) * D, D * 2,
-                                 &q_full);
-            }
-            for (int t0 = 0; t0 < tiles; t0 += 8) {
-                // lane: group lane % 4 of tile t0 + lane / 4
-                const int q = lane & 3, key0 = (g.tile0 + tile + t0 + (lane >> 2)) * kKeyTile, key = key0 + 16 * q;
-                int page = -1;
-                float ks = 0.f, vs = 0.f;
-                const int bk = key & ~(box - 1);  // the box's first key
-                const bool wanted = t0 + (lane >> 2) < tiles && bk + box > lo && bk < hi;
-                if (wanted) {
-                    page = b.table[(size_t)seq * b.max_pages + (key >> page_shift)];
-                    if (page < 0 || page >= b.num_pages) {
-                        paged::record_invalid(b.ws);
-                        page = -1;
-                    }
+        auto walk = [&]() {
+            for (; it < count;) {
+                const int per_head = g.units / b.Hkv, head = unit / per_head, row = unit % per_head * kRowTile;
+                const int rows = min(kRowTile, g.n * G - row);
+                const int lo = max(0, g.ctx + row / G - p.window + 1), hi = g.ctx + (row + rows - 1) / G + 1;
+                const int tiles = min(g.tiles - tile, count - it);  // of this unit, in this piece
+                // its query rows, once the consumers have turned the last unit's into operands
+                if (units > 0 && !__all_sync(0xffffffffu, wait(&q_empty, (uint32_t)(units - 1) & 1u, b.ws, &lost, 3))) return;
+                if (lane == 0) sm100::mbar_arrive_expect_tx(&q_full, (uint32_t)rows * D * 2);
+                __syncwarp();
+                if (lane < rows) {
+                    const int r = row + lane;
+                    sm100::bulk_load(qbuf + lane * D * 2, p.q + ((size_t)(g.row0 + r / G) * b.H + head * G + r % G) * D, D * 2,
+                                     &q_full);
                 }
-                const size_t at = (size_t)max(page, 0) * b.Hkv + head;
-                if (page >= 0) ks = p.ks[at], vs = p.vs[at];
-                const bool ok = page >= 0 && key + 16 > lo && key < hi;
-                const int leads = page >= 0 && key == bk;
-                const uint32_t oks = __ballot_sync(0xffffffffu, ok);
-                const int c1 = (int)((at << page_shift) + (key & (b.page - 1)));
-                for (int t = 0; t < min(8, tiles - t0); ++t, ++it) {
-                    const bool k_leads = __shfl_sync(0xffffffffu, leads, 4 * t + q) != 0 && lane < 4;
-                    const int k_c1 = __shfl_sync(0xffffffffu, c1, 4 * t + q);
-                    fill(&tm_k, k_leads, k_c1);
-                    if ((lane >> 2) == t) {
-                        Meta &mt = meta[it % kMeta];
-                        mt.ks[q] = ks;
-                        mt.lv[q] = ok ? log2f(vs) : 0.f;
-                        if (q == 0) {
-                            mt.ok = (int)((oks >> (4 * t)) & 0xfu);
-                            mt.key0 = key0;
-                            const int left = g.tiles - 1 - (tile + t0 + t);
-                            mt.flags = (tile + t0 + t == 0 ? 1 : 0) | (left == 0 ? 2 : 0) | (t0 + t == 0 ? 4 : 0);
-                            mt.row0 = g.row0, mt.ctx = g.ctx, mt.head = head;
-                            mt.row = row, mt.rows = rows, mt.left = left;
+                ++units;
+                for (int t0 = 0; t0 < tiles; t0 += 8) {
+                    // lane: group lane % 4 of tile t0 + lane / 4
+                    const int q = lane & 3, key0 = (g.tile0 + tile + t0 + (lane >> 2)) * kKeyTile, key = key0 + 16 * q;
+                    int page = -1;
+                    float ks = 0.f, vs = 0.f;
+                    const int bk = key & ~(box - 1);  // the box's first key
+                    const bool wanted = t0 + (lane >> 2) < tiles && bk + box > lo && bk < hi;
+                    if (wanted) {
+                        page = b.table[(size_t)seq * b.max_pages + (key >> page_shift)];
+                        if (page < 0 || page >= b.num_pages) {
+                            paged::record_invalid(b.ws);
+                            page = -1;
                         }
                     }
-                    filled();
-                    if (it > 0) {
-                        fill(&tm_v, v_leads, v_c1);
+                    const size_t at = (size_t)max(page, 0) * b.Hkv + head;
+                    if (page >= 0) ks = p.ks[at], vs = p.vs[at];
+                    const bool ok = page >= 0 && key + 16 > lo && key < hi;
+                    const int leads = page >= 0 && key == bk;
+                    const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+                    const int c1 = (int)((at << page_shift) + (key & (b.page - 1)));
+                    for (int t = 0; t < min(8, tiles - t0); ++t, ++it) {
+                        const bool k_leads = __shfl_sync(0xffffffffu, leads, 4 * t + q) != 0 && lane < 4;
+                        const int k_c1 = __shfl_sync(0xffffffffu, c1, 4 * t + q);
+                        if (!fill(&tm_k, k_leads, k_c1)) return;
+                        if ((lane >> 2) == t) {
+                            Meta &mt = meta[it % kMeta];
+                            mt.ks[q] = ks;
+                            mt.lv[q] = ok ? log2f(vs) : 0.f;
+                            if (q == 0) {
+                                mt.ok = (int)((oks >> (4 * t)) & 0xfu);
+                                mt.key0 = key0;
+                                const int left = g.tiles - 1 - (tile + t0 + t);
+                                mt.flags = (tile + t0 + t == 0 ? 1 : 0) | (left == 0 ? 2 : 0) | (t0 + t == 0 ? 4 : 0);
+                                mt.row0 = g.row0, mt.ctx = g.ctx, mt.head = head;
+                                mt.row = row, mt.rows = rows, mt.left = left;
+                            }
+                        }
                         filled();
+                        if (it > 0) {
+                            if (!fill(&tm_v, v_leads, v_c1)) return;
+                            filled(it == 1);
+                        }
+                        v_leads = k_leads, v_c1 = k_c1;
                     }
-                    v_leads = k_leads, v_c1 = k_c1;
+                }
+                tile = 0;
+                ++unit;
+                if (unit == g.units && it < count) {
+                    unit = 0;
+                    do g = geometry(p, ++seq); while (g.units == 0);
                 }
             }
-            tile = 0;
-            ++unit;
-            if (unit == g.units && it < count) {
-                unit = 0;
-                do g = geometry(p, ++seq); while (g.units == 0);
-            }
-        }
-        fill(&tm_v, v_leads, v_c1);
-        filled();
+            if (fill(&tm_v, v_leads, v_c1)) filled(count == 1);
+        };
+        walk();
+        if (held >= 0) give_back(full + held, &lost);
         // no copy is in flight when the CTA ends
         for (int k = 0; k < kSlots; ++k) {  // the slots' last uses, oldest first
             if (uses > 0 || k < slot) {
                 const int x = uses > 0 ? (slot + k) % kSlots : k;
-                wait(full + x, (uint32_t)(x < slot ? uses : uses - 1) & 1u, b.ws, 1);
+                drain_wait(full + x, (uint32_t)(x < slot ? uses : uses - 1) & 1u);
             }
         }
-        wait(&q_full, (uint32_t)(units - 1) & 1u, b.ws, 1);
+        if (units > 0) drain_wait(&q_full, (uint32_t)(units - 1) & 1u);
         return;
     }
 
@@ -364,20 +412,20 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
     int pos[2];
     int pos_first = 0, pos_last = 0, unit_first = 0, slot = 0;
     uint32_t phase = 0;
-    bool alive = true;
+    bool alive = true;  // this thread has won all its waits
     auto take = [&]() {  // the next slot of the ring, full
-        if (alive) alive = wait(full + slot, phase, b.ws, 2);
+        if (alive) alive = wait(full + slot, phase, b.ws, &lost, 2);
         return ring + slot * C::kSlotBytes;
     };
     auto release = [&]() {
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(empty + slot);
+        if (lane == 0 && alive) sm100::mbar_arrive(empty + slot);
         if (++slot == kSlots) slot = 0, phase ^= 1u;
     };
     // A unit's rows as f16 operands, each row times a power of two that brings its largest exponent to 2^13: every bf16
     // down to 2^-27 of it is a normal f16.  Warp w converts the 64 channels of step w.
     auto load_queries = [&](int rows, uint32_t turn) {
-        if (alive) alive = wait(&q_full, turn & 1u, b.ws, 4);
+        if (alive) alive = wait(&q_full, turn & 1u, b.ws, &lost, 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = quad + 8 * h;
@@ -411,7 +459,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
             }
         }
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&q_empty);
+        if (lane == 0 && alive) sm100::mbar_arrive(&q_empty);
         consumer_sync();
     };
     // raw scores of this warp's 16 keys of the next tile
@@ -443,10 +491,13 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
         release();
     };
     uint32_t units = 0;
-    if (alive) alive = wait(full, 0, b.ws, 2);  // tile 0's k, and with it its meta
+    if (alive) alive = wait(full, 0, b.ws, &lost, 2);  // tile 0's k, and with it its meta
     load_queries(meta[0].rows, units++);
     scores(s);
-    for (int it = 0; it < count; ++it) {
+    // Whether some consumer has lost a wait, settled at a barrier: the branches below that hold barriers go by a tile's
+    // meta, which only a won wait has brought.
+    bool held_up = bar_any(1, kConsumers, !alive);
+    for (int it = 0; it < count && !held_up; ++it) {
         const Meta &mt = meta[it % kMeta];
         if (mt.flags & 4) {  // the unit's first tile in this piece: its sums are empty
             unit_first = mt.flags & 1;
@@ -498,7 +549,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
         float sn[2][4] = {};
         if (it + 1 < count) {
             if (mt.left == 0) {  // another unit follows: every warp is done with the old operands
-                if (alive) alive = wait(full + slot, phase, b.ws, 2);
+                if (alive) alive = wait(full + slot, phase, b.ws, &lost, 2);
                 load_queries(meta[(it + 1) % kMeta].rows, units++);
             }
             scores(sn);
@@ -531,7 +582,8 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
 #pragma unroll
             for (int t = 0; t < kNt; ++t) acc[t][0] *= f[0], acc[t][1] *= f[0], acc[t][2] *= f[1], acc[t][3] *= f[1];
         }
-        consumer_sync();
+        held_up = bar_any(1, kConsumers, !alive);  // P is there, and with it the next tile's meta
+        if (held_up) break;
         const uint8_t *st = take();
 
         // O += P V for this warp's channels: 16 keys a step, the thread's kNt channels of four of them
@@ -625,7 +677,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
                 if (j == 0) lsum[warp][quad + 8 * h] = l[h];
             }
-            consumer_sync();
+            held_up = bar_any(1, kConsumers, !alive);
             const bool whole = unit_first && last;
             float *slot = parts + ((size_t)cta * 2 + (unit_first ? 1 : 0)) * part_floats(kRowTile, D);
             if (!whole && unit_first)  // the unit began here and goes on: the later CTAs with a part of it
@@ -634,7 +686,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
             for (int h = 0; h < 2; ++h) {
                 const int r = quad + 8 * h;
                 const float lt = (lsum[0][r] + lsum[1][r]) + (lsum[2][r] + lsum[3][r]);
-                if (r >= urows || !alive) continue;
+                if (r >= urows || held_up) continue;
                 const int c0 = warp * kSlice + 2 * kNt * j;  // 2 kNt contiguous channels
                 if (whole) {
                     const float o = lt == 0.f ? 0.f : sm100::ex2_approx(finite_or_0(mv[h])) / lt;
@@ -664,6 +716,12 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[nt][e] = sn[nt][e];
+    }
+    if (held_up) {
+        plan = {0, 0, 0, 0, 0};
+        for (int r = tid; r < 2 * kRowTile; r += kConsumers)
+            *reinterpret_cast<float4 *>(parts + ((size_t)cta * 2 + r / kRowTile) * part_floats(kRowTile, D) + 4 * (r % kRowTile)) =
+                make_float4(0.f, 0.f, 0.f, 1.f);
     }
     if (tid == 0) plans[cta] = plan;
 }
@@ -750,6 +808,7 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
 #pragma unroll
             for (int x = 0; x < kVec; ++x)
                 v0[k][x] = (reinterpret_cast<const float4 *>(part(c, k) + 4 * R + r * D) + lane)[32 * x];
+        if (__any_sync(0xffffffffu, st.w != 0.f)) continue;  // a part was lost
         float m = st.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -792,6 +851,7 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
         // a half warp: every 64th part, four channels a lane; all loads before the sums
         float4 v[kBatch], st[kBatch];
         float m = -INFINITY, mv = -INFINITY, l = 0.f;
+        bool gone = false;  // a part was lost
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
             const int k = 2 * kWarps * x + 2 * warp + (lane >> 4);
@@ -802,7 +862,7 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
         }
         // m over the parts, then mv relative to it
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) m = fmaxf(m, st[x].x);
+        for (int x = 0; x < kBatch; ++x) m = fmaxf(m, st[x].x), gone |= st[x].w != 0.f;
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
         if (lane == 0) red[warp][0] = m;
         __syncthreads();
@@ -831,8 +891,8 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         if (lane < 16) o[warp][lane] = t;
         if (lane == 0) red[warp][2] = l;
-        __syncthreads();
-        if (tid < 16) {
+        gone = __syncthreads_or(gone);
+        if (tid < 16 && !gone) {
             float lt = 0.f;
             t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -919,7 +979,9 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     __shared__ uint64_t q_full, s_full, s_free, p_full[2], pv_done[2], drain[2];
     __shared__ uint32_t tmem_holder;
     __shared__ long long scan[kWideThreads / 32];
-    __shared__ int nan_count, nan_key0[kNanTiles];
+    __shared__ int nan_count, nan_key0[kNanTiles], lost, held;
+    __shared__ int sent[2];  // tiles of k and v asked for by a warp 4 that gave up
+    __shared__ Plan plan;
     __shared__ Segment seg_s;
     __shared__ float2 trade[2][2][kWideRows];  // what the two threads of a row give each other
     const Batch &b = p.b;
@@ -938,6 +1000,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 mbar_init(p_full + i, kSoftmax), mbar_init(pv_done + i, 1), mbar_init(drain + i, 1);
             }
             mbar_init(&q_full, kSoftmax), mbar_init(&s_full, 1), mbar_init(&s_free, kSoftmax);
+            lost = 0, held = 0, sent[0] = -1, plan = {0, 0, 0, 0, 0};
             mbar_fence_init();
         }
     }
@@ -968,7 +1031,6 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     }
     const uint32_t tmem = tmem_holder;
     const int whole = units / n_ctas * n_ctas, rest = units - whole, cuts = rest > 0 ? n_ctas / rest : 1;
-    if (tid == 0) plans[cta] = {0, 0, 0, 0, 0};
 
     int n = 0;          // tiles done before this segment: the phase of every barrier
     bool alive = true;
@@ -1017,8 +1079,8 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
 
         if (warp == 4) {
             // ------------------------------------------------------------ pages by TMA
-            const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile);
-            for (int t0 = 0; t0 < tiles; t0 += 8) {
+            const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile), named = hook(b.ws);
+            for (int t0 = 0; t0 < tiles && alive; t0 += 8) {
                 const int q = lane & 3, key0 = (seg.tile0 + t0 + (lane >> 2)) * kKeyTile, key = key0 + 16 * q;
                 int page = -1;
                 float ks = 0.f, vs = 0.f;
@@ -1039,7 +1101,11 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     const int i = n + t0 + t, slot = i % kRing;
                     const uint32_t parity = (uint32_t)(i / kRing - 1) & 1u, bytes = (uint32_t)__popc(leaders & (0xfu << (4 * t))) * box * D;
                     const bool lead = leads && (lane >> 2) == t;
-                    if (i >= kRing && alive) alive = wait(k_free + slot, parity, b.ws, 10);
+                    alive = __all_sync(0xffffffffu, i < kRing || wait(k_free + slot, parity, b.ws, &lost, 10));
+                    if (!alive) {
+                        if (lane == 0) sent[0] = sent[1] = i;
+                        break;
+                    }
                     if (lane == 0) mbar_expect(k_full + slot, bytes);
                     __syncwarp();
 #pragma unroll
@@ -1053,14 +1119,21 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(k_full + slot);
-                    if (i >= kRing && alive) alive = wait(rv_free + slot, parity, b.ws, 11);
+                    alive = __all_sync(0xffffffffu, i < kRing || wait(rv_free + slot, parity, b.ws, &lost, 11));
+                    if (!alive) {
+                        if (lane == 0) sent[0] = i + 1, sent[1] = i;
+                        break;
+                    }
                     if (lane == 0) mbar_expect(rv_full + slot, bytes);
                     __syncwarp();
 #pragma unroll
                     for (int x = 0; x < D / 128; ++x)
                         if (lead) tma_load_2d(smem + C::kOffRawV + slot * C::kRaw + x * C::kRawHalf + q * 2048, &tm_v, rv_full + slot, x * 128, c1);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(rv_full + slot);
+                    if (i == 0 && named == cta + 1)
+                        held = 1;
+                    else if (lane == 0)
+                        mbar_arrive(rv_full + slot);
                 }
             }
         } else if (warp == 7 || warp >= 12) {
@@ -1070,9 +1143,9 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             const int cw = warp == 7 ? 0 : warp - 11, row = (cw & 1) * 32 + lane, c0 = (cw >> 1) * (D / 64);
             for (int t = 0; t < tiles; ++t) {
                 const int i = n + t, raw = i % kRing, slot = i & 1;
-                if (alive) alive = wait(rv_full + raw, (uint32_t)(i / kRing) & 1u, b.ws, 12);
-                if (t == 0 && alive) alive = wait(&q_full, (uint32_t)round & 1u, b.ws, 28);  // q has left this place
-                if (i >= 2 && alive) alive = wait(v_free + slot, (uint32_t)(i / 2 - 1) & 1u, b.ws, 13);
+                if (alive) alive = wait(rv_full + raw, (uint32_t)(i / kRing) & 1u, b.ws, &lost, 12);
+                if (t == 0 && alive) alive = wait(&q_full, (uint32_t)round & 1u, b.ws, &lost, 28);  // q has left this place
+                if (i >= 2 && alive) alive = wait(v_free + slot, (uint32_t)(i / 2 - 1) & 1u, b.ws, &lost, 13);
                 const Meta &mt = meta[i % kMeta];
                 const int key0 = mt.key0, key = key0 + row;
                 const bool in = ((mt.ok >> (row >> 4)) & 1) && key >= seg.lo && key < seg.hi;
@@ -1107,7 +1180,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0 && alive) {
                     mbar_arrive(v_full + slot);
                     mbar_arrive(rv_free + raw);
                 }
@@ -1117,10 +1190,11 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             const uint32_t idesc = umma_idesc_e4m3(kWideRows, kKeyTile);
             for (int t = 0; t < tiles; ++t) {
                 const int i = n + t, slot = i % kRing;
-                if (t == 0 && alive) alive = wait(&q_full, (uint32_t)round & 1u, b.ws, 16);
-                if (alive) alive = wait(k_full + slot, (uint32_t)(i / kRing) & 1u, b.ws, 17);
-                if (i >= 1 && alive) alive = wait(&s_free, (uint32_t)(i - 1) & 1u, b.ws, 18);
-                __syncwarp();
+                if (t == 0 && alive) alive = wait(&q_full, (uint32_t)round & 1u, b.ws, &lost, 16);
+                if (alive) alive = wait(k_full + slot, (uint32_t)(i / kRing) & 1u, b.ws, &lost, 17);
+                if (i >= 1 && alive) alive = wait(&s_free, (uint32_t)(i - 1) & 1u, b.ws, &lost, 18);
+                alive = __all_sync(0xffffffffu, alive);
+                if (!alive) break;
                 tc_fence_after();
                 const uint64_t kd = umma_desc_sw128(smem_u32(smem + C::kOffRawK + slot * C::kRaw));
 #pragma unroll
@@ -1138,9 +1212,10 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             const uint32_t idesc = umma_idesc_f16(kWideRows, D) | (1u << 16);  // v's channels are contiguous
             for (int t = 0; t < tiles; ++t) {
                 const int i = n + t, slot = i & 1;
-                if (alive) alive = wait(p_full + slot, (uint32_t)(i / 2) & 1u, b.ws, 19);
-                if (alive) alive = wait(v_full + slot, (uint32_t)(i / 2) & 1u, b.ws, 20);
-                __syncwarp();
+                if (alive) alive = wait(p_full + slot, (uint32_t)(i / 2) & 1u, b.ws, &lost, 19);
+                if (alive) alive = wait(v_full + slot, (uint32_t)(i / 2) & 1u, b.ws, &lost, 20);
+                alive = __all_sync(0xffffffffu, alive);
+                if (!alive) break;
                 tc_fence_after();
                 const uint64_t vd = umma_desc_mn_noswizzle(smem_u32(smem + C::kOffV + slot * C::kF16), 128, 1024);
 #pragma unroll
@@ -1237,7 +1312,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
 #pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
                 const int i = n + t, pb = i & 1;
-                if (alive) alive = wait(&s_full, (uint32_t)i & 1u, b.ws, 21);
+                if (alive) alive = wait(&s_full, (uint32_t)i & 1u, b.ws, &lost, 21);
                 __syncwarp();
                 tc_fence_after();
                 const Meta &mt = meta[i % kMeta];
@@ -1248,7 +1323,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     tmem_ld32(tmem + lane_off + C::kColS + (uint32_t)(32 * half), ra);
                     tmem_wait_ld();
                     tc_fence_before();
-                    mbar_arrive(&s_free);
+                    if (alive) mbar_arrive(&s_free);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = f2_make(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1]));
                 }
@@ -1295,7 +1370,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 if (__any_sync(0xffffffffu, move)) {
                     // O holds the tiles before: wait for the last of them, then scale in place, half of the channels a
                     // thread (a row moves after its first tile)
-                    if (alive) alive = wait(pv_done + ((i - 1) & 1), (uint32_t)((i - 1) / 2) & 1u, b.ws, 22);
+                    if (alive) alive = wait(pv_done + ((i - 1) & 1), (uint32_t)((i - 1) / 2) & 1u, b.ws, &lost, 22);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -1333,7 +1408,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 l2[0] = f2_add(l2[0], l2[1]);
                 l += f2_lo(l2[0]) + f2_hi(l2[0]);
                 // P's buffer was last read by the product of tile i - 2
-                if (i >= 2 && alive) alive = wait(pv_done + pb, (uint32_t)(i / 2 - 1) & 1u, b.ws, 23);
+                if (i >= 2 && alive) alive = wait(pv_done + pb, (uint32_t)(i / 2 - 1) & 1u, b.ws, &lost, 23);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
@@ -1341,26 +1416,27 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     tmem_st8(tmem + lane_off + C::kColP + (uint32_t)(pb * 32 + half * 16 + g * 8), pk[g]);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(p_full + pb);
+                if (alive) mbar_arrive(p_full + pb);
             }
             const int last = n + tiles - 1;
-            if (alive) alive = wait(pv_done + (last & 1), (uint32_t)(last / 2) & 1u, b.ws, 24);
+            if (alive) alive = wait(pv_done + (last & 1), (uint32_t)(last / 2) & 1u, b.ws, &lost, 24);
             __syncwarp();
             tc_fence_after();
-            const float2 other = swap(make_float2(l, alive ? 1.f : 0.f));
-            l = half == 0 ? l + other.x : other.x + l;
-            alive = alive && other.y != 0.f;
+            const float other = swap(make_float2(l, 0.f)).x;
+            l = half == 0 ? l + other : other + l;
+            // Of these 32 rows; a role that gave up said so before what it does next could reach them.
+            const bool held_up = bar_any(1 + quarter, 64, !alive || *(volatile int *)&lost != 0);
             const int bad = min(nan_count, kNanTiles);
             const bool is_whole = seg.parts == 1;
             float *slot = parts + (size_t)cta * part_floats(kWideRows, D);
             const float o_scale = l == 0.f ? 0.f : ex2_approx(finite_or_0(mv)) / l;
-            if (!is_whole && live && alive && half == 0) *reinterpret_cast<float4 *>(slot + 4 * r) = make_float4(m, mv, l, 0.f);
+            if (!is_whole && live && !held_up && half == 0) *reinterpret_cast<float4 *>(slot + 4 * r) = make_float4(m, mv, l, 0.f);
 #pragma unroll 1
             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 uint32_t o[32];
                 tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)c, o);
                 tmem_wait_ld();
-                if (live && alive)
+                if (live && !held_up)
                     for (int k = 0; k < bad; ++k)  // channels of NaN values that this row sees (noted tiles only, a few)
                         for (int e = max(nan_key0[k], lo); e <= min(nan_key0[k] + kKeyTile - 1, hi); ++e) {
                             const int page = b.table[(size_t)seg.seq * b.max_pages + e / b.page];
@@ -1385,7 +1461,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 for (int k = 0; k < 8; ++k) {  // four rows at a time, eight lanes each
                     const int rr = 4 * k + (lane >> 3), x = lane & 7, at = quarter * 32 + rr;
                     const uint4 w = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((x ^ (rr & 7)) << 4));
-                    if (at < seg.rows && alive) {
+                    if (at < seg.rows && !held_up) {
                         if (is_whole) {
                             const int gr = seg.row + at;
                             *reinterpret_cast<uint2 *>(
@@ -1398,8 +1474,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     }
                 }
             }
-            if (tid == 0 && !is_whole && seg.part == 0)
-                plans[cta] = {(short)seg.parts, (short)seg.rows, seg.row0, seg.row, seg.head};
+            if (tid == 0 && !is_whole && seg.part == 0) plan = {(short)seg.parts, (short)seg.rows, seg.row0, seg.row, seg.head};
             tc_fence_before();
         }
         n += tiles;
@@ -1408,16 +1483,20 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     __syncwarp();
     if (warp == 5 || warp == 6) {
         umma_commit_warp(drain + (warp - 5));
-        wait(drain + (warp - 5), 0, b.ws, 25);
+        drain_wait(drain + (warp - 5), 0);
     }
-    if (warp == 4)
-        for (int i = max(0, n - kRing); i < n; ++i) {
-            wait(k_full + i % kRing, (uint32_t)(i / kRing) & 1u, b.ws, 26);
-            wait(rv_full + i % kRing, (uint32_t)(i / kRing) & 1u, b.ws, 27);
-        }
+    if (warp == 4) {
+        if (held) give_back(rv_full, &lost);
+        const int k_sent = sent[0] < 0 ? n : sent[0], v_sent = sent[0] < 0 ? n : sent[1];
+        for (int i = max(0, k_sent - kRing); i < k_sent; ++i) drain_wait(k_full + i % kRing, (uint32_t)(i / kRing) & 1u);
+        for (int i = max(0, v_sent - kRing); i < v_sent; ++i) drain_wait(rv_full + i % kRing, (uint32_t)(i / kRing) & 1u);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (lost && tid < kWideRows)
+        *reinterpret_cast<float4 *>(parts + (size_t)cta * part_floats(kWideRows, D) + 4 * tid) = make_float4(0.f, 0.f, 0.f, 1.f);
+    if (tid == 0) plans[cta] = lost ? Plan{0, 0, 0, 0, 0} : plan;
     if (warp == 5) tmem_dealloc(tmem, 512);
 }
 

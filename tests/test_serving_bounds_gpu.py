@@ -1,10 +1,13 @@
 """The serving operators (rglru_add_rmsnorm and its neighbours) at the ends of what their calls allow: counts near
 2^31, probabilities far below a row's largest, waits that run out, batches that name rows twice, and the forms that
 a call picks by its size.  Worlds, oracle and bars as in test_serving_gpu.py."""
+import time
+
 import pytest
 import torch
 
 from lm_causal_depthwise_b200 import api
+from test_serving_gpu import World
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +33,41 @@ def test_add_rmsnorm_counts_rows_up_to_the_type():
     for i in range(0, M - tail, 1 << 27):
         part = out[i:min(i + (1 << 27), M - tail)]
         assert torch.equal(part.amin(0), row[0]) and torch.equal(part.amax(0), row[0])
+
+
+# --------------------------------------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("ctx,new,H,Hkv,unit,skipped", [
+    ([6000, 40, 3], [1, 1, 1], 8, 1, 0, [0]),                # 16 rows at a time: the piece that begins a cut unit
+    ([6000, 40, 3], [1, 1, 1], 8, 1, 1, [0]),                # a piece in its middle
+    ([100] * 40, [2] * 40, 4, 2, 0, None),                   # whole units of one CTA
+    ([3000, 20, 90], [40, 50, 64], 2, 1, 0, [0]),            # 128 rows at a time: a part of a cut unit
+    ([3000, 20, 90], [40, 50, 64], 2, 1, 1, [0]),
+    ([70] * 160, [20] * 160, 2, 1, 0, [0, 148])])            # a whole unit, and the CTA's next one
+def test_paged_attention_bounded_wait(ctx, new, H, Hkv, unit, skipped):
+    """The test hook makes a CTA keep back its first tile of values: the waits for it run out, the call ends with
+    RGLRU_ERR_TIMEOUT in the device status, the rows that it held up are not written (whatever earlier calls left in the
+    workspace) and all others are as ever, as is the next call."""
+    w, other = World(61, ctx, new, H, Hkv, 128, 16), World(62, [900, 4000, 1], [30, 2, 1], 8, 2, 128, 32)
+    ws = api.new_workspace(api.paged_attention_workspace_size(8, 2, 128))
+    q, batch, cache = w.q.to(dev), w.batch(), w.cache()
+    ref = api.paged_attention(q, batch, cache, workspace=ws)
+    api.paged_attention(other.q.to(dev), other.batch(), other.cache(), workspace=ws)
+    assert api.device_status(ws) == api.OK
+    out = torch.full_like(ref, 55.0)
+    api.debug_suppress_publish(ws, unit)
+    t0 = time.time()
+    api.paged_attention(q, batch, cache, out=out, workspace=ws)
+    assert api.device_status(ws) == api.ERR_TIMEOUT
+    assert time.time() - t0 < 60
+    api.debug_suppress_publish(ws, -1)
+    kept = (out.view(w.rows, H, 128) == 55).all(2)                       # rows of a token and head
+    assert torch.equal(out.view(w.rows, H, 128)[~kept], ref.view(w.rows, H, 128)[~kept])
+    if skipped is None:
+        assert kept[0, 0] and kept.sum() < kept.numel() / 4
+    else:
+        want = torch.zeros(w.rows, dtype=torch.bool, device=dev)
+        for i in skipped:
+            want[w.cu[i]:w.cu[i + 1]] = True
+        assert torch.equal(kept, want[:, None].expand(-1, H))
+    assert torch.equal(api.paged_attention(q, batch, cache, workspace=ws), ref)
+    assert api.device_status(ws) == api.OK
