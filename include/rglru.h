@@ -558,11 +558,20 @@ RGLRU_API rglru_status rglru_add_rmsnorm_e4m3(int M, int N, int group, const voi
  * those), any N up to 2^20, K up to 2^20.  The weights' integers and x enter
  * the products exactly, sums are fp32, the output is rounded once.  There is no
  * workspace, and no status word: a device-side wait that ran out (2 s, more
- * than 16 rows only) would leave NaN in the outputs it held up.
+ * than 16 rows only) leaves NaN in the outputs it held up.
  */
 RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group, const void *A, const float *A_scale,
                                        int a_group, const void *W, const void *W_scale, const float *bias, void *out,
                                        cudaStream_t stream);
+
+/*
+ * Test hook for that wait (never used by a normal call): in the next
+ * rglru_linear_w4 calls of this thread with more than 16 rows, CTA `unit`
+ * keeps back an arrival on its first block of weights, as
+ * rglru_debug_suppress_publish does for the calls with a workspace.
+ * unit = -1 turns it off.
+ */
+RGLRU_API rglru_status rglru_debug_linear_w4_withhold(int unit);
 
 /*
  * The paged cache and the batch, for both calls below:

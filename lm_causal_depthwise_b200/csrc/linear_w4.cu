@@ -25,6 +25,7 @@ constexpr int kBlockK = 128;
 
 struct W4Args {
     int M, N, K, group_shift, a_shift;  // log2 of the groups
+    int withhold;  // test hook: 1 + the CTA that keeps an arrival back, 0 = none
     const void *A;
     const float *A_scale;
     const uint8_t *W;
@@ -311,7 +312,9 @@ __device__ __forceinline__ const float *peer(const float *x, int rank)
     asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(x), "r"(rank));
     return reinterpret_cast<const float *>(a);
 }
-// A wait that gives up after 2 s returns false; the caller goes on without waiting again and its outputs become NaN.
+// A wait that gives up after 2 s returns false.  Who gave up waits no more and passes the barriers of the CTA and the
+// cluster with the others, but arrives on no mbarrier and starts nothing: every arrival stands for a wait that was won, so
+// those behind run out of their waits too, up to the threads of the outputs, which become NaN.
 __device__ __noinline__ bool w4_wait_slow(uint64_t *bar, uint32_t parity)
 {
     const uint64_t t0 = sm100::globaltimer();
@@ -460,7 +463,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
             if (warp >= 5) {
                 // ------------------------------------------------------------ weights to operands
                 for (int b = pass; b < end; ++b) {
+                    // a warp's verdict: its store to TMEM is one instruction, and the last block there may be in use
                     if (turn > 0 && alive) alive = w4_wait(a_free + slot, (uint32_t)(turn - 1) & 1u);
+                    alive = __all_sync(0xffffffffu, alive);
                     auto write = [&](uint32_t *words) {  // a register queue needs its place known when compiled
                         uint32_t r[32];
 #pragma unroll
@@ -471,7 +476,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
                         }
                         load_w(words);
                         __syncwarp();
-                        tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kTcColA + (uint32_t)(slot * 64 + ubox * 32), r);
+                        if (alive) tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kTcColA + (uint32_t)(slot * 64 + ubox * 32), r);
                     };
                     tc_fence_after();
                     switch (at) {
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
                     at = (at + 1) % kTcAhead;
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(a_full + slot);
+                    if (alive && !(tid == 5 * 32 && round == 0 && b == 0 && p.withhold == (int)blockIdx.x + 1)) mbar_arrive(a_full + slot);
                     next_slot();
                 }
             } else if (warp == 4) {
@@ -493,7 +498,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
                 for (int b = pass; b < end; ++b) {
                     if (alive) alive = w4_wait(a_full + slot, (uint32_t)turn & 1u);
                     if (set_turn > 0 && alive) alive = w4_wait(d_free + set, (uint32_t)(set_turn - 1) & 1u);
-                    __syncwarp();
+                    alive = __all_sync(0xffffffffu, alive);
+                    if (!alive) break;
                     tc_fence_after();
                     const uint64_t xd = umma_desc_sw128(smem_u32(xs + (b - (once ? 0 : pass)) * C::kX));
 #pragma unroll
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
                     }
                     tmem_wait_ld();
                     tc_fence_before();
-                    mbar_arrive(d_free + set);
+                    if (alive) mbar_arrive(d_free + set);
                     next_set();
                 }
             }
@@ -605,6 +611,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
 }
 
 constexpr int kSms = 148;
+thread_local int withheld = 0;  // of the calls of this thread
 
 template <int NT, int R, bool kE4m3, bool kVec>
 rglru_status launch_few(const W4Args &p, cudaStream_t stream)
@@ -699,7 +706,7 @@ extern "C" RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group
                       args::span(bias, bias ? 4 * (size_t)N : 0)}))
         return RGLRU_ERR_INVALID_ARG;
     auto log2i = [](int v) { int s = 0; while ((1 << s) < v) ++s; return s; };
-    const W4Args p = {M, N, K, log2i(group), A_scale ? log2i(a_group) : 0, A, A_scale, static_cast<const uint8_t *>(W),
+    const W4Args p = {M, N, K, log2i(group), A_scale ? log2i(a_group) : 0, withheld, A, A_scale, static_cast<const uint8_t *>(W),
                       static_cast<const uint16_t *>(W_scale), bias, static_cast<__nv_bfloat16 *>(out)};
     // Up to 16 rows the first kernel is as fast or faster at every size measured (16 rows of 12288 x 4096: 35 us both;
     // 8 rows of 7680 x 2560 13 us against 20; one row of 2560 x 2560 10 against 14).
@@ -709,4 +716,11 @@ extern "C" RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group
     case 3: return launch_tc<48>(p, stream);
     default: return launch_tc<64>(p, stream);
     }
+}
+
+extern "C" RGLRU_API rglru_status rglru_debug_linear_w4_withhold(int unit)
+{
+    if (unit < -1) return RGLRU_ERR_INVALID_ARG;
+    withheld = unit + 1;
+    return RGLRU_OK;
 }

@@ -3,11 +3,12 @@
 a call picks by its size.  Worlds, oracle and bars as in test_serving_gpu.py."""
 import time
 
+import numpy as np
 import pytest
 import torch
 
 from lm_causal_depthwise_b200 import api
-from test_serving_gpu import World
+from test_serving_gpu import World, _w4_case
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,28 @@ def test_paged_attention_bounded_wait(ctx, new, H, Hkv, unit, skipped):
         assert torch.equal(kept, want[:, None].expand(-1, H))
     assert torch.equal(api.paged_attention(q, batch, cache, workspace=ws), ref)
     assert api.device_status(ws) == api.OK
+
+
+@pytest.mark.parametrize("M,N,K,unit", [(20, 1000, 2560, 0), (64, 20001, 1280, 5), (64, 70, 20480, 1)])
+def test_linear_w4_bounded_wait(M, N, K, unit):
+    """The test hook makes a CTA keep back an arrival on its first block of weights: the waits run out, the outputs of
+    its cluster (tiles of 128) are NaN and nothing else is touched, and the next call is as ever."""
+    A, _, W, s, b, _ = (t if t is None or not torch.is_tensor(t) else t.to(dev)
+                        for t in _w4_case(np.random.default_rng(8), M, N, K, 128, 0))
+    ref = api.linear_w4(A, W, s, b)
+    t0 = time.time()
+    api.debug_linear_w4_withhold(unit)
+    try:
+        got = api.linear_w4(A, W, s, b)
+    finally:
+        api.debug_linear_w4_withhold(-1)
+    torch.cuda.synchronize()
+    assert time.time() - t0 < 60
+    nan = got.isnan()
+    tiles = nan.all(0)
+    assert torch.equal(nan, tiles.expand(M, -1)) and tiles.any()
+    for n in range(0, N, 128):
+        assert tiles[n:n + 128].all() or not tiles[n:n + 128].any()
+    assert N < 128 or not tiles.all()
+    assert torch.equal(got[:, ~tiles], ref[:, ~tiles])
+    assert torch.equal(api.linear_w4(A, W, s, b), ref)
