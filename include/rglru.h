@@ -221,10 +221,8 @@ RGLRU_API rglru_status rglru_get_device_status(void *workspace, cudaStream_t str
  * RGLRU_ERR_TIMEOUT instead of hanging; on a decode workspace, CTA `unit` of
  * the next rglru_decode_step calls keeps its half of the gate GEMM's operand
  * from its peer CTA, whose wait runs out the same way (the call then takes a
- * few seconds); on an attention workspace, CTA `unit` of the next
- * rglru_paged_attention calls keeps back its first tile of values.  unit = -1
- * turns it off.  The flag lives in the workspace header and is enqueued on
- * `stream`.
+ * few seconds).  unit = -1 turns it off.  The flag lives in the workspace
+ * header and is enqueued on `stream`.
  */
 RGLRU_API rglru_status rglru_debug_suppress_publish(void *workspace, int unit, cudaStream_t stream);
 
@@ -565,15 +563,6 @@ RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group, const voi
                                        cudaStream_t stream);
 
 /*
- * Test hook for that wait (never used by a normal call): in the next
- * rglru_linear_w4 calls of this thread with more than 16 rows, CTA `unit`
- * keeps back an arrival on its first block of weights, as
- * rglru_debug_suppress_publish does for the calls with a workspace.
- * unit = -1 turns it off.
- */
-RGLRU_API rglru_status rglru_debug_linear_w4_withhold(int unit);
-
-/*
  * The paged cache and the batch, for both calls below:
  *   k_cache, v_cache [num_pages, Hkv, page_size, head_dim] e4m3 codes and
  *     k_scale, v_scale [num_pages, Hkv] fp32: one scale for each page and head;
@@ -644,6 +633,15 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
                                              const int32_t *ctx_len, const int32_t *block_table, const void *k_cache,
                                              const float *k_scale, const void *v_cache, const float *v_scale, void *out,
                                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Test hook for the bounded waits of the serving calls (never used by a normal
+ * call): in the next calls of this thread, CTA `unit` keeps back an arrival,
+ * so that the waits for it run out: rglru_linear_w4 with more than 16 rows
+ * that of its first block of weights, rglru_paged_attention that of its first
+ * tile of values (the call then takes a few seconds).  unit = -1 turns it off.
+ */
+RGLRU_API rglru_status rglru_debug_withhold(int unit);
 
 /*
  * The five serving calls with their parameters in a block, for callers to whom

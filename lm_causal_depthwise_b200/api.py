@@ -32,8 +32,8 @@ SYMBOLS = ("rglru_version", "rglru_status_string", "rglru_workspace_size", "rglr
            "rglru_mqa_vt_size", "rglru_mqa_rope", "rglru_mqa_attention", "rglru_mqa_block_workspace_size",
            "rglru_mqa_block_prefill", "rglru_mqa_decode_workspace_size", "rglru_mqa_decode_step",
            "rglru_mqa_residual_block_workspace_size", "rglru_mqa_residual_block_prefill", "rglru_carry_scan",
-           "rglru_add_rmsnorm", "rglru_add_rmsnorm_e4m3", "rglru_linear_w4", "rglru_debug_linear_w4_withhold",
-           "rglru_paged_append", "rglru_paged_attention_workspace_size", "rglru_paged_attention", "rglru_serving_call")
+           "rglru_add_rmsnorm", "rglru_add_rmsnorm_e4m3", "rglru_linear_w4", "rglru_paged_append",
+           "rglru_paged_attention_workspace_size", "rglru_paged_attention", "rglru_debug_withhold", "rglru_serving_call")
 
 _lib = None
 
@@ -127,14 +127,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rglru_add_rmsnorm_e4m3.argtypes = [i, i, i, vp, vp, vp, f, vp, vp, vp, vp]
     lib.rglru_linear_w4.restype = i
     lib.rglru_linear_w4.argtypes = [i, i, i, i, vp, vp, i, vp, vp, vp, vp, vp]
-    lib.rglru_debug_linear_w4_withhold.restype = i
-    lib.rglru_debug_linear_w4_withhold.argtypes = [i]
     lib.rglru_paged_append.restype = i
     lib.rglru_paged_append.argtypes = [i] * 10 + [vp] * 4 + [f] + [vp] * 6 + [sz, vp]
     lib.rglru_paged_attention_workspace_size.restype = sz
     lib.rglru_paged_attention_workspace_size.argtypes = [i, i, i]
     lib.rglru_paged_attention.restype = i
     lib.rglru_paged_attention.argtypes = [i] * 11 + [f] + [vp] * 10 + [sz, vp]
+    lib.rglru_debug_withhold.restype = i
+    lib.rglru_debug_withhold.argtypes = [i]
     lib.rglru_serving_call.restype = i
     lib.rglru_serving_call.argtypes = [i, ctypes.c_char_p]
     _lib = lib
@@ -987,10 +987,11 @@ def linear_w4(A, W, W_scale, bias=None, A_scale=None, out=None) -> torch.Tensor:
     return out
 
 
-def debug_linear_w4_withhold(unit: int) -> None:
-    st = load().rglru_debug_linear_w4_withhold(int(unit))
+def debug_withhold(unit: int) -> None:
+    """Test hook of linear_w4's and paged_attention's bounded waits (rglru_debug_withhold)."""
+    st = load().rglru_debug_withhold(int(unit))
     if st != OK:
-        raise RGLRUError(st, "rglru_debug_linear_w4_withhold")
+        raise RGLRUError(st, "rglru_debug_withhold")
 
 
 @dataclass

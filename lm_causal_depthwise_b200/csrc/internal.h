@@ -87,6 +87,10 @@ rglru_status decode_step(const PrefillArgs &a);
 
 inline rglru_status cuda_status(cudaError_t e) { return e == cudaSuccess ? RGLRU_OK : RGLRU_ERR_CUDA; }
 
+// Test hook of the serving operators (rglru_debug_withhold): 1 + the CTA that keeps an arrival back, 0 = none
+// (serving_call.cu).
+extern thread_local int debug_withheld;
+
 // Argument checks of the serving operators: alignment, and overlap of the byte ranges of a call
 // (an empty range meets nothing).
 namespace args {

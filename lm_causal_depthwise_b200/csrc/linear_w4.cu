@@ -611,7 +611,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) rglru_linear_w4_tc_kernel(const
 }
 
 constexpr int kSms = 148;
-thread_local int withheld = 0;  // of the calls of this thread
 
 template <int NT, int R, bool kE4m3, bool kVec>
 rglru_status launch_few(const W4Args &p, cudaStream_t stream)
@@ -706,7 +705,7 @@ extern "C" RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group
                       args::span(bias, bias ? 4 * (size_t)N : 0)}))
         return RGLRU_ERR_INVALID_ARG;
     auto log2i = [](int v) { int s = 0; while ((1 << s) < v) ++s; return s; };
-    const W4Args p = {M, N, K, log2i(group), A_scale ? log2i(a_group) : 0, withheld, A, A_scale, static_cast<const uint8_t *>(W),
+    const W4Args p = {M, N, K, log2i(group), A_scale ? log2i(a_group) : 0, debug_withheld, A, A_scale, static_cast<const uint8_t *>(W),
                       static_cast<const uint16_t *>(W_scale), bias, static_cast<__nv_bfloat16 *>(out)};
     // Up to 16 rows the first kernel is as fast or faster at every size measured (16 rows of 12288 x 4096: 35 us both;
     // 8 rows of 7680 x 2560 13 us against 20; one row of 2560 x 2560 10 against 14).
@@ -716,11 +715,4 @@ extern "C" RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group
     case 3: return launch_tc<48>(p, stream);
     default: return launch_tc<64>(p, stream);
     }
-}
-
-extern "C" RGLRU_API rglru_status rglru_debug_linear_w4_withhold(int unit)
-{
-    if (unit < -1) return RGLRU_ERR_INVALID_ARG;
-    withheld = unit + 1;
-    return RGLRU_OK;
 }

@@ -19,6 +19,7 @@ struct AttendArgs {
     Batch b;
     int window;
     float scale;
+    int withhold;  // test hook: 1 + the CTA that keeps an arrival back, 0 = none
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;
     const float *ks, *vs;
@@ -90,9 +91,10 @@ __device__ __forceinline__ Geometry geometry(const AttendArgs &p, int i)
 
 // ------------------------------------------------------------------------------------------------ pieces
 // A wait gives up after 2 s, or once another of its CTA has (`lost`, in shared memory); the first to give up records it.
-// Who gave up waits no more and passes the CTA's barriers with the others, but arrives on no mbarrier and starts no copy
-// or product: every arrival stands for a wait that was won, so the others run out of theirs as well, and none takes a slot
-// that is half full for a full one.  The rows held up are not written, and the CTA's parts say that they are not there.
+// Who gave up waits no more and passes the CTA's barriers with the others, but arrives on no mbarrier (the 128-row
+// kernel's softmax threads excepted) and starts no copy or product: an arrival stands for a wait that was won, so the
+// others run out of theirs as well, and none takes a slot that is half full for a full one.  The rows held up are not
+// written, and the CTA's parts say that they are not there.
 __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, WsHeader *ws, volatile int *lost, int where)
 {
     const uint64_t t0 = sm100::globaltimer();
@@ -117,14 +119,8 @@ __device__ __noinline__ void drain_wait(uint64_t *bar, uint32_t parity)
     while (!sm100::mbar_try_wait_sleep(bar, parity, 20000u) && sm100::globaltimer() - t0 < kTimeoutNs) {
     }
 }
-// Test hook (rglru_debug_suppress_publish): the CTA it names keeps back the arrival on its first tile of v until the
-// waits for it have run out.  (The flag is read long before that: its way from memory would show in every call.)
-__device__ __forceinline__ int hook(const WsHeader *ws)
-{
-    int unit;
-    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(unit) : "l"(&ws->debug_unit_plus1));  // volatile: stays where it is called
-    return unit;
-}
+// Test hook: the CTA that keeps back the arrival on its first tile of v (AttendArgs::withhold) makes it here, once the
+// waits for it have run out.
 __device__ __noinline__ void give_back(uint64_t *bar, volatile int *lost)
 {
     const uint64_t t0 = sm100::globaltimer();
@@ -285,7 +281,6 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
 
     if (warp == kConsumers / 32) {
         // ---------------------------------------------------------------- producer
-        const int named = hook(b.ws);
         const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile);
         int seq = where[0], unit = where[1], tile = where[2], it = 0, units = 0, slot = 0, uses = 0;
         Geometry g = where_g;
@@ -305,7 +300,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
         };
         auto filled = [&](bool first_v = false) {
             __syncwarp();
-            if (first_v && named == cta + 1)
+            if (first_v && p.withhold == cta + 1)
                 held = slot;
             else if (lane == 0)
                 sm100::mbar_arrive(full + slot);
@@ -1079,7 +1074,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
 
         if (warp == 4) {
             // ------------------------------------------------------------ pages by TMA
-            const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile), named = hook(b.ws);
+            const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile);
             for (int t0 = 0; t0 < tiles && alive; t0 += 8) {
                 const int q = lane & 3, key0 = (seg.tile0 + t0 + (lane >> 2)) * kKeyTile, key = key0 + 16 * q;
                 int page = -1;
@@ -1130,7 +1125,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     for (int x = 0; x < D / 128; ++x)
                         if (lead) tma_load_2d(smem + C::kOffRawV + slot * C::kRaw + x * C::kRawHalf + q * 2048, &tm_v, rv_full + slot, x * 128, c1);
                     __syncwarp();
-                    if (i == 0 && named == cta + 1)
+                    if (i == 0 && p.withhold == cta + 1)
                         held = 1;
                     else if (lane == 0)
                         mbar_arrive(rv_full + slot);
@@ -1323,7 +1318,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     tmem_ld32(tmem + lane_off + C::kColS + (uint32_t)(32 * half), ra);
                     tmem_wait_ld();
                     tc_fence_before();
-                    if (alive) mbar_arrive(&s_free);
+                    mbar_arrive(&s_free);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = f2_make(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1]));
                 }
@@ -1416,16 +1411,18 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     tmem_st8(tmem + lane_off + C::kColP + (uint32_t)(pb * 32 + half * 16 + g * 8), pk[g]);
                 tmem_wait_st();
                 tc_fence_before();
-                if (alive) mbar_arrive(p_full + pb);
+                mbar_arrive(p_full + pb);
             }
             const int last = n + tiles - 1;
             if (alive) alive = wait(pv_done + (last & 1), (uint32_t)(last / 2) & 1u, b.ws, &lost, 24);
             __syncwarp();
             tc_fence_after();
-            const float other = swap(make_float2(l, 0.f)).x;
-            l = half == 0 ? l + other : other + l;
-            // Of these 32 rows; a role that gave up said so before what it does next could reach them.
-            const bool held_up = bar_any(1 + quarter, 64, !alive || *(volatile int *)&lost != 0);
+            // Whether these 32 rows were held up.  A softmax thread that gave up goes on arriving (256 of them, whose
+            // guards would cost 0.4 us), so `lost` counts too: it is set before an arrival that could mislead these rows.
+            const bool mine_up = !alive || *(volatile int *)&lost != 0;
+            const float2 other = swap(make_float2(l, mine_up ? 1.f : 0.f));
+            l = half == 0 ? l + other.x : other.x + l;
+            const bool held_up = __any_sync(0xffffffffu, mine_up || other.y != 0.f);
             const int bad = min(nan_count, kNanTiles);
             const bool is_whole = seg.parts == 1;
             float *slot = parts + (size_t)cta * part_floats(kWideRows, D);
@@ -1563,7 +1560,7 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
 {
     const AttendArgs p = {{rows, S, H, Hkv, head_dim, page_size, num_pages, max_pages, max_new, max_total, cu_tokens,
                            ctx_len, block_table, static_cast<WsHeader *>(workspace)},
-                          window, scale, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
+                          window, scale, debug_withheld, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
                           static_cast<const uint8_t *>(v_cache), k_scale, v_scale, static_cast<__nv_bfloat16 *>(out)};
     const size_t need = rglru_paged_attention_workspace_size(H, Hkv, head_dim);
     const rglru_status c = paged::check_batch(p.b, k_cache, k_scale, v_cache, v_scale, workspace_bytes, need);

@@ -1,8 +1,17 @@
 // serving_call.cu -- the serving calls with their parameters in a block.
 //
 // An interpreter converts each argument of a foreign call by itself (ctypes: 0.25 us an argument, 22 of them for
-// rglru_paged_append), and packs a struct in one call.  Host code only.
+// rglru_paged_append), and packs a struct in one call.  Host code only, and with it the serving operators' test hook.
 #include "internal.h"
+
+thread_local int rglru::debug_withheld = 0;
+
+extern "C" RGLRU_API rglru_status rglru_debug_withhold(int unit)
+{
+    if (unit < -1) return RGLRU_ERR_INVALID_ARG;
+    rglru::debug_withheld = unit + 1;
+    return RGLRU_OK;
+}
 
 extern "C" RGLRU_API rglru_status rglru_serving_call(rglru_call call, const void *args)
 {

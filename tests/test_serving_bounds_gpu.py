@@ -55,12 +55,14 @@ def test_paged_attention_bounded_wait(ctx, new, H, Hkv, unit, skipped):
     api.paged_attention(other.q.to(dev), other.batch(), other.cache(), workspace=ws)
     assert api.device_status(ws) == api.OK
     out = torch.full_like(ref, 55.0)
-    api.debug_suppress_publish(ws, unit)
     t0 = time.time()
-    api.paged_attention(q, batch, cache, out=out, workspace=ws)
+    api.debug_withhold(unit)
+    try:
+        api.paged_attention(q, batch, cache, out=out, workspace=ws)
+    finally:
+        api.debug_withhold(-1)
     assert api.device_status(ws) == api.ERR_TIMEOUT
     assert time.time() - t0 < 60
-    api.debug_suppress_publish(ws, -1)
     kept = (out.view(w.rows, H, 128) == 55).all(2)                       # rows of a token and head
     assert torch.equal(out.view(w.rows, H, 128)[~kept], ref.view(w.rows, H, 128)[~kept])
     if skipped is None:
@@ -82,11 +84,11 @@ def test_linear_w4_bounded_wait(M, N, K, unit):
                         for t in _w4_case(np.random.default_rng(8), M, N, K, 128, 0))
     ref = api.linear_w4(A, W, s, b)
     t0 = time.time()
-    api.debug_linear_w4_withhold(unit)
+    api.debug_withhold(unit)
     try:
         got = api.linear_w4(A, W, s, b)
     finally:
-        api.debug_linear_w4_withhold(-1)
+        api.debug_withhold(-1)
     torch.cuda.synchronize()
     assert time.time() - t0 < 60
     nan = got.isnan()
