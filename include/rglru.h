@@ -615,8 +615,10 @@ RGLRU_API size_t rglru_paged_attention_workspace_size(int H, int Hkv, int head_d
  * q, out [rows, H * head_dim] bf16 (q as rglru_paged_append gives it); window
  * >= 1 (2^30 or more reaches every position); scale > 0.  Scores, sums and the
  * output's accumulation are fp32; the probabilities enter the second product
- * as f16.  With max_new * H / Hkv <= 32 q enters the first product exactly; with
- * more (chunks) as two e4m3 terms, exact for channels down to 2^-9 of the row's
+ * as f16, those far below the row's largest (times its page's v_scale) off by
+ * up to 2^-40 of it, in chunks over at most 2^20 keys by up to 2^-32.  With
+ * max_new * H / Hkv <= 32 q enters the first product exactly; with more
+ * (chunks) as two e4m3 terms, exact for channels down to 2^-9 of the row's
  * largest and off by at most 2^-17 of it below.  A row with no key (bad pages
  * only) gives zeros, a row whose q has an infinity or NaN gives NaN.
  * num_pages * Hkv * page_size and rows * H are below 2^31 (else

@@ -19,6 +19,7 @@ struct AttendArgs {
     Batch b;
     int window;
     float scale;
+    float top, raise;  // 128 rows at a time: log2 of the largest P at its reference, and how far P may pass it
     int withhold;  // test hook: 1 + the CTA that keeps an arrival back, 0 = none
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;
@@ -34,6 +35,7 @@ constexpr int kRowTile = 16, kKeyTile = 64, kMinTiles = 2, kManyTiles = 10;
 constexpr int kConsumers = 128, kThreads = kConsumers + 32;
 constexpr int kSms = 148, kMaxCtas = 3 * kSms;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr float kTop = 15.f;  // log2 of the largest P (f16 ends at 2^16)
 constexpr size_t align_up_d(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 struct Meta {                // of one tile in the ring, written by the producer
@@ -188,9 +190,10 @@ __device__ __forceinline__ int piece_of(long long total, long long t, int n) { r
 // and the next one's products fill it.
 // Codes turn into f16 operands exactly, in registers (the e4m3 form of this mma is slower: it runs as conversions and
 // f16 products, 5.0 cycles against 2.2).  k's scale multiplies the scores; v's enters the exponent: P holds
-// 2^(s - m + log2 vs - mv) with mv the running maximum of s - m + log2 vs, beside the softmax's own maximum m and sum
-// l = sum 2^(s - m), so that P keeps f16's bits whatever the pages' scales (mv is relative to m: a large score would
-// swallow log2 vs).
+// 2^(s - m + log2 vs - mv) with mv the running maximum of s - m + log2 vs less 15, beside the softmax's own maximum m and
+// sum l = sum 2^(s - m), so that P keeps f16's bits whatever the pages' scales (mv is relative to m: a large score would
+// swallow log2 vs).  The 15 put the largest P at f16's upper end: a key keeps its bits down to 2^-29 of the largest and is
+// off by at most 2^-40 of it below.
 // Measured, 10 heads of 256 to one key head: 256 sequences over 2048 keys 65 us with the launch and the join (4.1 TB/s
 // of codes; a CTA's tile takes 1.7 us and more also out of L2, which is the consumers' chain); one sequence over 131072
 // keys 29 us, of which 6 to the first tile's end and 7 the join.
@@ -539,7 +542,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
             tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], 2));
             if (j == 0) reinterpret_cast<float *>(&wmax[quad + 8 * h])[warp] = tmax[h];
         }
-        if (lane == 0) reinterpret_cast<float *>(&wlv)[warp] = lv;
+        if (lane == 0) reinterpret_cast<float *>(&wlv)[warp] = lv - kTop;
         consumer_sync();
         float sn[2][4] = {};
         if (it + 1 < count) {
@@ -684,12 +687,12 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
                 if (r >= urows || held_up) continue;
                 const int c0 = warp * kSlice + 2 * kNt * j;  // 2 kNt contiguous channels
                 if (whole) {
-                    const float o = lt == 0.f ? 0.f : sm100::ex2_approx(finite_or_0(mv[h])) / lt;
+                    const float o = lt == 0.f ? 0.f : 1.f / lt, o2 = sm100::ex2_approx(finite_or_0(mv[h]));
                     uint32_t w[kNt];
 #pragma unroll
                     for (int t = 0; t < kNt; ++t) {
                         const int e = 2 * t / kNt, x = 2 * t % kNt;  // channel 2 t of the thread's 2 kNt
-                        w[t] = pack_bf16(acc[x][2 * h + e] * o, acc[x + 1][2 * h + e] * o);
+                        w[t] = pack_bf16(acc[x][2 * h + e] * o * o2, acc[x + 1][2 * h + e] * o * o2);
                     }
                     const int row = urow + r;
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)(row0 + row / G) * b.H + head * G + row % G) * D + c0);
@@ -833,11 +836,11 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
                 t[x].x += v.x * fk, t[x].y += v.y * fk, t[x].z += v.z * fk, t[x].w += v.w * fk;
             }
         }
-        const float g = l == 0.f ? 0.f : sm100::ex2_approx(vz) / l;
+        const float g = l == 0.f ? 0.f : 1.f / l, g2 = sm100::ex2_approx(vz);
         uint2 *dst = reinterpret_cast<uint2 *>(out_row(pl, r)) + lane;
 #pragma unroll
         for (int x = 0; x < kVec; ++x)
-            dst[32 * x] = make_uint2(pack_bf16(t[x].x * g, t[x].y * g), pack_bf16(t[x].z * g, t[x].w * g));
+            dst[32 * x] = make_uint2(pack_bf16(t[x].x * g * g2, t[x].y * g * g2), pack_bf16(t[x].z * g * g2, t[x].w * g * g2));
     }
 
     for (int item = blockIdx.x; item < total[1]; item += gridDim.x) {
@@ -895,8 +898,9 @@ __global__ void __launch_bounds__(kJoinThreads) rglru_paged_combine_kernel(const
                 const float4 x = o[w][tid];
                 lt += red[w][2], t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
             }
-            const float f = lt == 0.f ? 0.f : sm100::ex2_approx(vz) / lt;
-            reinterpret_cast<uint2 *>(out_row(pl, r) + ch)[tid] = make_uint2(pack_bf16(t.x * f, t.y * f), pack_bf16(t.z * f, t.w * f));
+            const float f = lt == 0.f ? 0.f : 1.f / lt, f2 = sm100::ex2_approx(vz);
+            reinterpret_cast<uint2 *>(out_row(pl, r) + ch)[tid] =
+                make_uint2(pack_bf16(t.x * f * f2, t.y * f * f2), pack_bf16(t.z * f * f2, t.w * f * f2));
         }
         __syncthreads();
     }
@@ -926,7 +930,8 @@ bool encode_pool(CUtensorMap *m, const uint8_t *base, const Batch &b)
 // longest wait; P stays f16, since two e4m3 terms of it would lose the keys below 2^-18 of a row's largest, whose sum
 // counts in a long cache.
 // Exponents, scales and their references as in the 16-row kernel, with the references raised only when a row's maximum
-// passes them by 2^8 (P up to 2^8 keeps f16's bits), since moving O means a pass through TMEM.
+// passes them by 2^raise, since moving O means a pass through TMEM; P is 2^top at its reference, top + raise = 15, and a
+// key is off by at most 2^-(25 + top) of the row's largest.
 // A CTA takes whole units, and the last ones (fewer than CTAs) are cut into equal ranges of tiles: at most one part a
 // CTA, joined as above.
 // Measured: five chunks of up to 256 tokens, 10 heads of 256, 2048 keys each: 45 us with the launch and the join, 330
@@ -1357,10 +1362,10 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                                         fmaxf(og.x - mz + mt.lv[2 - 2 * half], og.y - mz + mt.lv[3 - 2 * half]));
                 float f = 1.f;
                 bool move = false;
-                if (top > mv + kRaise || (mv == -INFINITY && top > mv)) {
+                if (top > mv + (p.raise + p.top) || (mv == -INFINITY && top > mv)) {
                     move = mv != -INFINITY;
-                    if (move) f = ex2_approx(mv - top);
-                    mv = top;
+                    if (move) f = ex2_approx(mv - top + p.top);
+                    mv = top - p.top;
                 }
                 if (__any_sync(0xffffffffu, move)) {
                     // O holds the tiles before: wait for the last of them, then scale in place, half of the channels a
@@ -1426,7 +1431,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
             const int bad = min(nan_count, kNanTiles);
             const bool is_whole = seg.parts == 1;
             float *slot = parts + (size_t)cta * part_floats(kWideRows, D);
-            const float o_scale = l == 0.f ? 0.f : ex2_approx(finite_or_0(mv)) / l;
+            const float o_scale = l == 0.f ? 0.f : 1.f / l, o_scale2 = ex2_approx(finite_or_0(mv));
             if (!is_whole && live && !held_up && half == 0) *reinterpret_cast<float4 *>(slot + 4 * r) = make_float4(m, mv, l, 0.f);
 #pragma unroll 1
             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
@@ -1450,7 +1455,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        w[e] = is_whole ? __float_as_uint(__uint_as_float(o[4 * x + e]) * o_scale) : o[4 * x + e];
+                        w[e] = is_whole ? __float_as_uint(__uint_as_float(o[4 * x + e]) * o_scale * o_scale2) : o[4 * x + e];
                     *reinterpret_cast<uint4 *>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 __syncwarp();
@@ -1533,7 +1538,14 @@ rglru_status launch(const AttendArgs &p, cudaStream_t stream)
     }
     const rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_wide_kernel<D>), W::kSmem, wide_flag);
     if (st != RGLRU_OK) return st;
-    rglru_paged_attention_wide_kernel<D><<<kSms, kWideThreads, W::kSmem, stream>>>(p, tm_k, tm_v);
+    // What keys below f16's range lose is at most 2^-(25 + top) a key: over 2^20 keys 2^-12 of the largest with a raise of
+    // 2^8, so beyond them the reference follows every maximum (2^-10 over 2^30 keys).  Five chunks of up to 256 tokens over
+    // 2048 keys: 44.9 us against 48.8.
+    const int64_t reach = (int64_t)p.window + p.b.max_new < p.b.max_total ? (int64_t)p.window + p.b.max_new : p.b.max_total;
+    AttendArgs a = p;
+    a.raise = reach <= (1 << 20) ? 8.f : 0.f;
+    a.top = kTop - a.raise;
+    rglru_paged_attention_wide_kernel<D><<<kSms, kWideThreads, W::kSmem, stream>>>(a, tm_k, tm_v);
     if (cudaGetLastError() != cudaSuccess) return RGLRU_ERR_CUDA;
     return launch_join<D, kWideRows>(p, kSms, stream);
 }
@@ -1560,7 +1572,7 @@ RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, in
 {
     const AttendArgs p = {{rows, S, H, Hkv, head_dim, page_size, num_pages, max_pages, max_new, max_total, cu_tokens,
                            ctx_len, block_table, static_cast<WsHeader *>(workspace)},
-                          window, scale, debug_withheld, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
+                          window, scale, 0.f, 0.f, debug_withheld, static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(k_cache),
                           static_cast<const uint8_t *>(v_cache), k_scale, v_scale, static_cast<__nv_bfloat16 *>(out)};
     const size_t need = rglru_paged_attention_workspace_size(H, Hkv, head_dim);
     const rglru_status c = paged::check_batch(p.b, k_cache, k_scale, v_cache, v_scale, workspace_bytes, need);

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from lm_causal_depthwise_b200 import api
-from test_serving_gpu import World, _w4_case
+from oracle import serving as O
+from test_serving_gpu import World, _attend, _np, _w4_case, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +100,32 @@ def test_linear_w4_bounded_wait(M, N, K, unit):
     assert N < 128 or not tiles.all()
     assert torch.equal(got[:, ~tiles], ref[:, ~tiles])
     assert torch.equal(api.linear_w4(A, W, s, b), ref)
+
+
+# ------------------------------------------------------------------------------------ probabilities far below the largest
+@pytest.mark.parametrize("new,kw,far", [(1, {}, 28), (5, {}, 28), (40, {}, 20.5), (40, dict(max_total=(1 << 20) + 1000), 28)])
+def test_paged_attention_flat_tail_behind_a_heavy_key(new, kw, far):
+    """The first key takes nearly all of the probability and has no values; what the row gets is the sum of the others, each
+    2^-far of it: far below f16's smallest value where the largest probability is 1.  Bar as in test_serving_gpu.py: a
+    probability of 2^-far keeps f16's bits (2^-29 of the largest and above; 2^-21 in chunks over at most 2^20 keys)."""
+    w = World(63, [300], [new], 2, 1, 128, 16)
+    w.ks[:], w.vs[:] = 2.0 ** -8, 2.0 ** -7
+    w.k[:] = 0
+    w.k[..., 0] = -256
+    w.k[w.table[0, 0], 0, 0, 0] = 0
+    w.v = np.where(w.v == 0, 1.0, np.abs(w.v))
+    w.v[w.table[0, 0], 0, 0] = 0
+    q = torch.zeros(new, 2, 128)
+    q[..., 0] = 1
+    w.q = q.view(new, 256).to(bf)
+    scale = far * np.log(2)
+    if kw:
+        w.table = np.pad(w.table, ((0, 0), (0, kw["max_total"] // 16 + 1 - w.table.shape[1])), constant_values=-7)
+    got, ws = _attend(w, api.FULL_WINDOW, scale, **kw)
+    assert api.device_status(ws) == api.OK
+    want, size, smax = O.attention(_np(w.q).reshape(new, 2, 128), w.cu, w.ctx, w.table, w.k, w.ks, w.v, w.vs,
+                                   api.FULL_WINDOW, float(np.float32(scale)))
+    assert (want > 0).all() and want.max() < 2.0 ** (9 - far + 2)       # 340 keys of up to 448 / 128
+    # the exponential's argument: `far` with 24 bits and log2 e's rounding, together at most far 2^-23, so 2^-18 holds it
+    rel = 2.0 ** -11 + 2 * (128 / 16 + 8) * 2.0 ** -23 * smax + 2.0 ** -17
+    _within(_np(got).reshape(want.shape), want, 2.0 ** -8 * np.abs(want) + rel[..., None] * size, "tail")
