@@ -1042,19 +1042,29 @@ def _paged_args(batch: PagedBatch, cache: PagedCache, dev):
     return S, Hkv, D, ps, P, max_pages
 
 
-def _paged_workspace(workspace, need, dev):
-    if workspace is None:
-        workspace = new_workspace(need, dev)
+def _paged_workspace(workspace, dev):
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous, on {dev}")
     return workspace, workspace.numel() * workspace.element_size()
+
+
+def _paged_report(workspace, name: str, dev) -> None:
+    """Raises what the device recorded in the workspace of a call whose caller has none to read it from."""
+    with torch.cuda.device(dev):
+        if torch.cuda.is_current_stream_capturing():
+            return
+        st = device_status(workspace)
+    if st != OK:
+        raise RGLRUError(st, name)
 
 
 def paged_append(qkv, batch: PagedBatch, cache: PagedCache, rope_base: float = 10000.0, q_out=None,
                  workspace=None) -> torch.Tensor:
     """RoPE on the query and key heads of qkv [rows, (H + 2 Hkv) * D] bf16, the new keys and values into the
     cache's pages in 8 bits (rglru_paged_append, in place); returns the rotated queries [rows, H * D] bf16.
-    A device-side refusal (bad lengths or page numbers) is read with device_status(workspace)."""
+    A device-side refusal (bad lengths or page numbers) is read with device_status(workspace).  Without a workspace
+    the call makes one, waits for the device and raises the refusal itself; inside a capture it cannot, so a captured
+    call whose refusals matter is given one."""
     dev = qkv.device
     S, Hkv, D, ps, P, max_pages = _paged_args(batch, cache, dev)
     H = qkv.shape[1] // D - 2 * Hkv if qkv.dim() == 2 and D else 0
@@ -1066,11 +1076,14 @@ def paged_append(qkv, batch: PagedBatch, cache: PagedCache, rope_base: float = 1
         q_out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
     else:
         _need(q_out, "q_out", (rows, H * D), torch.bfloat16, dev)
-    workspace, nb = _paged_workspace(workspace, 4096, dev)
+    own = workspace is None
+    workspace, nb = _paged_workspace(new_workspace(4096, dev) if own else workspace, dev)
     _enqueue("rglru_paged_append", dev, rows, S, H, Hkv, D, ps, P, max_pages, batch.max_new, batch.max_total,
              qkv.data_ptr(), batch.cu_tokens.data_ptr(), batch.ctx_len.data_ptr(), batch.block_table.data_ptr(),
              rope_base, q_out.data_ptr(), cache.k.data_ptr(), cache.k_scale.data_ptr(), cache.v.data_ptr(),
              cache.v_scale.data_ptr(), workspace.data_ptr(), nb)
+    if own:
+        _paged_report(workspace, "rglru_paged_append", dev)
     return q_out
 
 
@@ -1085,7 +1098,8 @@ def paged_attention(q, batch: PagedBatch, cache: PagedCache, window: int = MQA_W
                     out=None, workspace=None) -> torch.Tensor:
     """Attention of the new tokens over the cache (rglru_paged_attention): q [rows, H * D] bf16 as paged_append
     returns it; a token attends the ``window`` positions that end at its own; scale 1 / sqrt(D) unless given.
-    Returns out [rows, H * D] bf16 (rows behind the last sequence are not written)."""
+    Returns out [rows, H * D] bf16 (rows behind the last sequence are not written).  The workspace and refusals as for
+    paged_append; without one the call also zero-fills up to 20 MB."""
     dev = q.device
     S, Hkv, D, ps, P, max_pages = _paged_args(batch, cache, dev)
     H = q.shape[1] // D if q.dim() == 2 and D else 0
@@ -1097,12 +1111,13 @@ def paged_attention(q, batch: PagedBatch, cache: PagedCache, window: int = MQA_W
         out = torch.empty((rows, H * D), dtype=torch.bfloat16, device=dev)
     else:
         _need(out, "out", (rows, H * D), torch.bfloat16, dev)
-    if workspace is None:
-        workspace = new_workspace(paged_attention_workspace_size(H, Hkv, D), dev)
-    workspace, nb = _paged_workspace(workspace, 0, dev)
+    own = workspace is None
+    workspace, nb = _paged_workspace(new_workspace(paged_attention_workspace_size(H, Hkv, D), dev) if own else workspace, dev)
     _enqueue("rglru_paged_attention", dev, rows, S, H, Hkv, D, ps, P, max_pages, batch.max_new, batch.max_total,
              min(int(window), FULL_WINDOW), D ** -0.5 if scale is None else scale, q.data_ptr(),
              batch.cu_tokens.data_ptr(), batch.ctx_len.data_ptr(), batch.block_table.data_ptr(), cache.k.data_ptr(),
              cache.k_scale.data_ptr(), cache.v.data_ptr(), cache.v_scale.data_ptr(), out.data_ptr(),
              workspace.data_ptr(), nb)
+    if own:
+        _paged_report(workspace, "rglru_paged_attention", dev)
     return out

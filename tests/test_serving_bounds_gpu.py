@@ -129,3 +129,37 @@ def test_paged_attention_flat_tail_behind_a_heavy_key(new, kw, far):
     # the exponential's argument: `far` with 24 bits and log2 e's rounding, together at most far 2^-23, so 2^-18 holds it
     rel = 2.0 ** -11 + 2 * (128 / 16 + 8) * 2.0 ** -23 * smax + 2.0 ** -17
     _within(_np(got).reshape(want.shape), want, 2.0 ** -8 * np.abs(want) + rel[..., None] * size, "tail")
+
+
+# ------------------------------------------------------------------------------------------- calls without a workspace
+def test_refusals_of_calls_without_a_workspace_are_raised():
+    """Nobody else can read the workspace that a call makes for itself: what the device refused is raised by the call, after
+    everything else was done; calls that are fine are as with a workspace, and capture."""
+    w = World(64, [20, 3, 40], [3, 2, 1], 2, 1, 128, 16)
+    q, qkv = w.q.to(dev), w.qkv.to(dev)
+    ws = api.new_workspace(api.paged_attention_workspace_size(2, 1, 128))
+    c0, c1 = w.cache(), w.cache()
+    ref_q = api.paged_append(qkv, w.batch(), c0, workspace=ws)
+    ref = api.paged_attention(q, w.batch(), c0, workspace=ws)
+    assert torch.equal(api.paged_append(qkv, w.batch(), c1), ref_q)
+    assert torch.equal(api.paged_attention(q, w.batch(), c1), ref)
+    good = w.batch()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = api.paged_attention(q, good, c1)
+    g.replay()
+    assert torch.equal(out, ref)
+
+    bad = w.batch()
+    bad.block_table[1, 0] = w.P                              # a page that is not there
+    for kw, rows in ((dict(block_table=bad.block_table), slice(3, 5)), (dict(max_new=2), slice(0, 3))):
+        q_out, out = torch.full_like(ref_q, 55.0), torch.full_like(ref, 55.0)
+        with pytest.raises(api.RGLRUError) as e:
+            api.paged_append(qkv, w.batch(**kw), w.cache(), q_out=q_out)
+        assert e.value.status == api.ERR_INVALID_ARG
+        with pytest.raises(api.RGLRUError) as e:
+            api.paged_attention(q, w.batch(**kw), c0, out=out)
+        assert e.value.status == api.ERR_INVALID_ARG
+        keep = torch.ones(w.rows, dtype=torch.bool, device=dev)
+        keep[rows] = False
+        assert torch.equal(out[keep], ref[keep]) and torch.equal(q_out[keep], ref_q[keep])
