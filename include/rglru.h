@@ -580,8 +580,11 @@ RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group, const voi
  * sequence whose lengths break the bounds is skipped, a page number outside the
  * pool is not touched (its tokens are not stored, or its keys not attended), and
  * RGLRU_ERR_INVALID_ARG is recorded in the workspace (rglru_get_device_status).
- * Rows behind cu_tokens[S] are left as they were.  1 <= rows <= 2^24,
- * S <= 65535, H <= 256 a multiple of Hkv <= 64, max_total <= 2^30.
+ * So is a cu_tokens that goes back somewhere (a negative count), without which
+ * no two sequences can name the same row; a row named twice holds what one of
+ * them or the other wrote.  Rows behind cu_tokens[S] are left as they were.
+ * 1 <= rows <= 2^24, S <= 65535, H <= 256 a multiple of Hkv <= 64, max_total <=
+ * 2^30.
  */
 
 /*
@@ -622,12 +625,11 @@ RGLRU_API size_t rglru_paged_attention_workspace_size(int H, int Hkv, int head_d
  * largest and off by at most 2^-17 of it below.  A row with no key (bad pages
  * only) gives zeros, a row whose q has an infinity or NaN gives NaN.
  * num_pages * Hkv * page_size and rows * H are below 2^31 (else
- * RGLRU_ERR_UNSUPPORTED).  Sequences whose rows overlap
- * are recorded as RGLRU_ERR_INVALID_ARG when they come to more rows than the
- * call has.  The workspace (up to 20 MB, whatever the batch) is zero-filled once
- * and not shared by calls that can overlap; a device-side wait that ran out
- * (2 s) is recorded there as RGLRU_ERR_TIMEOUT, and the rows it held up are not
- * written.
+ * RGLRU_ERR_UNSUPPORTED).  Sequences that name rows twice leave all rows
+ * unwritten where they come to far more rows than a call of chunks has.  The
+ * workspace (up to 20 MB, whatever the batch) is zero-filled once and not shared
+ * by calls that can overlap; a device-side wait that ran out (2 s) is recorded
+ * there as RGLRU_ERR_TIMEOUT, and the rows it held up are not written.
  */
 RGLRU_API rglru_status rglru_paged_attention(int rows, int S, int H, int Hkv, int head_dim, int page_size,
                                              int num_pages, int max_pages, int max_new, int max_total, int window,

@@ -1023,7 +1023,8 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
         if (w < warp) before += scan[w];
         all += scan[w];
     }
-    // More units than the rows hold: sequences that overlap, which no batch has.
+    // More units than the rows hold: sequences that name rows twice (cu goes back between them, so load_seq has recorded
+    // it); refused here too, so that the counts stay within the host's bounds.
     int units = (int)all;
     if (all > (long long)b.H * b.rows / kWideRows + (long long)b.S * b.Hkv) {
         units = 0;

@@ -163,3 +163,37 @@ def test_refusals_of_calls_without_a_workspace_are_raised():
         keep = torch.ones(w.rows, dtype=torch.bool, device=dev)
         keep[rows] = False
         assert torch.equal(out[keep], ref[keep]) and torch.equal(q_out[keep], ref_q[keep])
+
+
+# ----------------------------------------------------------------------------------------------- rows named twice
+@pytest.mark.parametrize("n", [4, 40])
+def test_paged_rows_named_by_two_sequences_are_recorded(n):
+    """cu_tokens goes back between two sequences that share rows: recorded by both calls, for single tokens as for chunks,
+    and the rows of the others are as ever."""
+    w = World(65, [20, 0, 33, 7], [n, 0, n, 5], 2, 1, 128, 16, pad=2)
+    cu = torch.tensor([0, n, 0, n, n + 5], dtype=torch.int32, device=dev)     # sequences 0 and 2 share rows 0 .. n - 1
+    one = api.PagedBatch(torch.tensor([n, n + 5], dtype=torch.int32, device=dev), w.batch().ctx_len[3:].clone(),
+                         w.batch().block_table[3:].clone(), max(n, 5), w.max_total)
+    q, qkv, c0, c1 = w.q.to(dev), w.qkv.to(dev), w.cache(), w.cache()
+    ws = api.new_workspace(api.paged_attention_workspace_size(2, 1, 128))
+    q_out, q_ref, out, ref = (torch.full_like(q, 55.0) for _ in range(4))
+    api.paged_append(qkv, w.batch(cu_tokens=cu), c0, q_out=q_out, workspace=ws)
+    assert api.device_status(ws) == api.ERR_INVALID_ARG
+    api.paged_attention(q, w.batch(cu_tokens=cu), c0, out=out, workspace=ws)
+    assert api.device_status(ws) == api.ERR_INVALID_ARG
+    api.paged_append(qkv, one, c1, q_out=q_ref, workspace=ws)
+    api.paged_attention(q, one, c1, out=ref, workspace=ws)
+    assert api.device_status(ws) == api.OK
+    assert torch.equal(q_out[n:], q_ref[n:]) and torch.equal(out[n:], ref[n:])
+    assert torch.isfinite(out[:n].float()).all() and not (out[:n] == 55).any()
+
+
+def test_paged_attention_many_sequences_on_the_same_rows_are_recorded():
+    """50 sequences name the same 3 rows: recorded, nothing outside those rows is touched."""
+    w = World(66, [30] * 100, [3, 0] * 50, 4, 1, 128, 16)
+    cu = torch.tensor(([0, 3] * 50)[:100] + [0], dtype=torch.int32, device=dev)
+    out = torch.full((w.rows, 512), 55.0, dtype=bf, device=dev)
+    ws = api.new_workspace(api.paged_attention_workspace_size(4, 1, 128))
+    api.paged_attention(w.q.to(dev), w.batch(cu_tokens=cu), w.cache(), out=out, workspace=ws)
+    assert api.device_status(ws) == api.ERR_INVALID_ARG
+    assert (out[3:] == 55).all() and torch.isfinite(out[:3].float()).all()
