@@ -147,7 +147,8 @@ rglru_status launch(int M, int N, int group, const void *x, const void *res, con
     // 32768 x 2560, bf16: one vector a thread and 1536 threads an SM 106 us (97% of the measured bandwidth with the
     // launch), 2048 threads 117, two vectors 113.  The e4m3 form has the maxima's shuffles to hide: two vectors and 2048
     // threads 111 us, one vector 123 to 131; 4099 x 4096 25 us against 31.
-    if (!kE4m3 && N <= 4096) return launch_vpt<1, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
+    if constexpr (!kE4m3)
+        if (N <= 4096) return launch_vpt<1, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
     if (N <= 2 * 4096) return launch_vpt<2, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
     return launch_vpt<4, kE4m3>(M, N, group, x, res, w, eps, res_out, out, out_scale, stream);
 }

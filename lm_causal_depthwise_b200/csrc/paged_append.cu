@@ -232,8 +232,9 @@ rglru_status launch(const AppendArgs &p, cudaStream_t stream)
     if (items <= 128) return launch<D, 2, 64>(p, rows, stream);
     if (items <= 256) return launch<D, 2, 128>(p, rows, stream);
     if (items <= 512) return launch<D, 2, 256>(p, rows, stream);
-    if (items <= 1024) return launch<D, 2, 512>(p, rows, stream);
-    return launch<D, 8, 256>(p, rows, stream);
+    if constexpr (D == 256)  // a page of 128 slots: twice 1024
+        if (items > 1024) return launch<D, 8, 256>(p, rows, stream);
+    return launch<D, 2, 512>(p, rows, stream);
 }
 
 }  // namespace
