@@ -9,7 +9,7 @@ import torch
 
 from lm_causal_depthwise_b200 import api
 from oracle import serving as O
-from test_serving_gpu import World, _attend, _np, _w4_case, _within
+from test_serving_gpu import World, _attend, _bf16, _check_attend, _check_norm, _check_w4, _np, _w4_case, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +197,33 @@ def test_paged_attention_many_sequences_on_the_same_rows_are_recorded():
     api.paged_attention(w.q.to(dev), w.batch(cu_tokens=cu), w.cache(), out=out, workspace=ws)
     assert api.device_status(ws) == api.ERR_INVALID_ARG
     assert (out[3:] == 55).all() and torch.isfinite(out[:3].float()).all()
+
+
+# ---------------------------------------------------------------------------------- the forms that a call picks by its size
+@pytest.mark.parametrize("M,N,group", [(3000, 2560, 0), (1500, 8200, 0), (700, 16384, 0), (1300, 5120, 128)])
+@pytest.mark.parametrize("with_residual", [True, False])
+def test_add_rmsnorm_more_rows_than_ctas(M, N, group, with_residual):
+    """Every CTA walks over several rows, in each count of vectors a thread."""
+    rng = np.random.default_rng(M)
+    x, w = _bf16(rng, M, N), torch.from_numpy((1 + 0.2 * rng.standard_normal(N)).astype(np.float32))
+    _check_norm(x, _bf16(rng, M, N, scale=4) if with_residual else None, w, 1e-6, group)
+
+
+@pytest.mark.parametrize("M", [1, 5, 8, 12])
+@pytest.mark.parametrize("N,K,group,a_group", [(4737, 256, 32, 0), (4800, 416, 32, 32), (7681, 640, 128, 128),
+                                               (7680, 2560, 128, 0), (5000, 288, 32, 0), (4737, 1152, 128, 64),
+                                               (6001, 192, 64, 64)])
+def test_linear_w4_two_row_tiles_a_cta(M, N, K, group, a_group):
+    """Few rows and many outputs: both counts of row tiles of x, both kinds of x, K in whole blocks of 128 and not."""
+    _check_w4(np.random.default_rng(M * 10 + K), M, N, K, group, a_group)
+
+
+@pytest.mark.parametrize("D,page,new", [(128, 16, 1), (256, 64, 1), (128, 32, 2)])
+def test_paged_attention_three_ctas_an_sm(D, page, new):
+    """More than 4440 tiles of keys: pieces over three CTAs an SM, with units cut between them."""
+    rng = np.random.default_rng(D + page)
+    ctx = rng.integers(380, 640, 150)
+    ctx[3] = 5000
+    w = World(67, ctx, [new] * 150, 8, 4, D, page)
+    _check_attend(w, api.FULL_WINDOW)
+    assert torch.equal(_attend(w, 700)[0], _check_attend(w, 700))
