@@ -39,7 +39,7 @@ rglru_add_rmsnorm_kernel(int M, int N, int group, const uint4 *__restrict__ x, c
     const int tid = threadIdx.x, nvec = N / 8;
     float4 wv[VPT][2];
     uint4 v[VPT], r[VPT];
-    auto load = [&](unsigned row) {
+    auto load = [&](int row) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int i = k * blockDim.x + tid;
@@ -59,8 +59,8 @@ rglru_add_rmsnorm_kernel(int M, int N, int group, const uint4 *__restrict__ x, c
         wv[k][1] = i < nvec ? w[2 * i + 1] : make_float4(0, 0, 0, 0);
     }
     int turn = 0;
-    // unsigned: the row after the last may lie past 2^31
-    for (unsigned row = blockIdx.x; row < (unsigned)M; row += gridDim.x, turn ^= 1) {
+    const int last = M - (int)gridDim.x;  // rows from here on are their CTA's last: the next one may lie past 2^31
+    for (int row = blockIdx.x;; row += gridDim.x, turn ^= 1) {
         uint4 h[VPT];
         float ss = 0.f;
 #pragma unroll
@@ -81,7 +81,7 @@ rglru_add_rmsnorm_kernel(int M, int N, int group, const uint4 *__restrict__ x, c
                 ss = fmaf(bf_hi(q[e]), bf_hi(q[e]), ss);
             }
         }
-        if (row + gridDim.x < (unsigned)M) load(row + gridDim.x);
+        if (row < last) load(row + gridDim.x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         // two turns: a row's sums are read while the next row's are written
@@ -117,6 +117,7 @@ rglru_add_rmsnorm_kernel(int M, int N, int group, const uint4 *__restrict__ x, c
                 }
             }
         }
+        if (row >= last) break;
     }
 }
 
