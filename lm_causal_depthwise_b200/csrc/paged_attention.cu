@@ -20,7 +20,7 @@ struct AttendArgs {
     int window;
     float scale;
     float top, raise;  // 128 rows at a time: log2 of the largest P at its reference, and how far P may pass it
-    int withhold;  // test hook: 1 + the CTA that keeps an arrival back, 0 = none
+    int withhold;  // test hook: 1 + the CTA that keeps back the arrival on its first tile of v, 0 = none
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;
     const float *ks, *vs;
@@ -114,22 +114,13 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, WsHeader *w
 {
     return sm100::mbar_try_wait(bar, parity) || wait_slow(bar, parity, ws, lost, where);
 }
-// For what is in flight when a CTA ends, whether or not a wait was lost.
+// For what is in flight when a CTA ends, whether or not a wait was lost (2 s also where the test hook keeps the arrival back
+// that would end the wait: the copy has landed by then).
 __device__ __noinline__ void drain_wait(uint64_t *bar, uint32_t parity)
 {
     const uint64_t t0 = sm100::globaltimer();
     while (!sm100::mbar_try_wait_sleep(bar, parity, 20000u) && sm100::globaltimer() - t0 < kTimeoutNs) {
     }
-}
-// Test hook: the CTA that keeps back the arrival on its first tile of v (AttendArgs::withhold) makes it here, once the
-// waits for it have run out.
-__device__ __noinline__ void give_back(uint64_t *bar, volatile int *lost)
-{
-    const uint64_t t0 = sm100::globaltimer();
-    while (*lost == 0 && sm100::globaltimer() - t0 < 2 * kTimeoutNs) {
-    }
-    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
-    __syncwarp();
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // barrier `id` of `count` threads; whether any of them has x
@@ -287,7 +278,6 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
         const int page_shift = 31 - __clz(b.page), box = min(b.page, kKeyTile);
         int seq = where[0], unit = where[1], tile = where[2], it = 0, units = 0, slot = 0, uses = 0;
         Geometry g = where_g;
-        int held = -1;  // slot whose arrival is kept back
         // a slot to fill: `boxes` of this lane's c1 (lanes 0 .. 3 with `leads`), k or v; false when the wait for it was lost
         auto fill = [&](const CUtensorMap *tm, bool leads, int c1) {
             if (uses > 0 && !__all_sync(0xffffffffu, wait(empty + slot, (uint32_t)(uses - 1) & 1u, b.ws, &lost, 0))) return false;
@@ -303,10 +293,7 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
         };
         auto filled = [&](bool first_v = false) {
             __syncwarp();
-            if (first_v && p.withhold == cta + 1)
-                held = slot;
-            else if (lane == 0)
-                sm100::mbar_arrive(full + slot);
+            if (lane == 0 && !(first_v && p.withhold == cta + 1)) sm100::mbar_arrive(full + slot);
             if (++slot == kSlots) slot = 0, ++uses;
         };
         bool v_leads = false;  // of the tile whose v comes next
@@ -382,7 +369,6 @@ rglru_paged_attention_kernel(const AttendArgs p, const __grid_constant__ CUtenso
             if (fill(&tm_v, v_leads, v_c1)) filled(count == 1);
         };
         walk();
-        if (held >= 0) give_back(full + held, &lost);
         // no copy is in flight when the CTA ends
         for (int k = 0; k < kSlots; ++k) {  // the slots' last uses, oldest first
             if (uses > 0 || k < slot) {
@@ -979,7 +965,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
     __shared__ uint64_t q_full, s_full, s_free, p_full[2], pv_done[2], drain[2];
     __shared__ uint32_t tmem_holder;
     __shared__ long long scan[kWideThreads / 32];
-    __shared__ int nan_count, nan_key0[kNanTiles], lost, held;
+    __shared__ int nan_count, nan_key0[kNanTiles], lost;
     __shared__ int sent[2];  // tiles of k and v asked for by a warp 4 that gave up
     __shared__ Plan plan;
     __shared__ Segment seg_s;
@@ -1000,7 +986,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                 mbar_init(p_full + i, kSoftmax), mbar_init(pv_done + i, 1), mbar_init(drain + i, 1);
             }
             mbar_init(&q_full, kSoftmax), mbar_init(&s_full, 1), mbar_init(&s_free, kSoftmax);
-            lost = 0, held = 0, sent[0] = -1, plan = {0, 0, 0, 0, 0};
+            lost = 0, sent[0] = -1, plan = {0, 0, 0, 0, 0};
             mbar_fence_init();
         }
     }
@@ -1131,10 +1117,7 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
                     for (int x = 0; x < D / 128; ++x)
                         if (lead) tma_load_2d(smem + C::kOffRawV + slot * C::kRaw + x * C::kRawHalf + q * 2048, &tm_v, rv_full + slot, x * 128, c1);
                     __syncwarp();
-                    if (i == 0 && p.withhold == cta + 1)
-                        held = 1;
-                    else if (lane == 0)
-                        mbar_arrive(rv_full + slot);
+                    if (lane == 0 && !(i == 0 && p.withhold == cta + 1)) mbar_arrive(rv_full + slot);
                 }
             }
         } else if (warp == 7 || warp >= 12) {
@@ -1489,7 +1472,6 @@ rglru_paged_attention_wide_kernel(const AttendArgs p, const __grid_constant__ CU
         drain_wait(drain + (warp - 5), 0);
     }
     if (warp == 4) {
-        if (held) give_back(rv_full, &lost);
         const int k_sent = sent[0] < 0 ? n : sent[0], v_sent = sent[0] < 0 ? n : sent[1];
         for (int i = max(0, k_sent - kRing); i < k_sent; ++i) drain_wait(k_full + i % kRing, (uint32_t)(i / kRing) & 1u);
         for (int i = max(0, v_sent - kRing); i < v_sent; ++i) drain_wait(rv_full + i % kRing, (uint32_t)(i / kRing) & 1u);
