@@ -575,9 +575,11 @@ RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group, const voi
  *     block_table[i, p / page_size]; entries that a call does not need
  *     (pages before the window, pages past the end) are not read and may hold anything.
  * max_new and max_total bound the lengths: cu_tokens[i + 1] - cu_tokens[i] <=
- * max_new, ctx_len[i] plus that <= max_total <= max_pages * page_size.  The
- * lengths and the table live on the device, so they are checked there: a
- * sequence whose lengths break the bounds is skipped, a page number outside the
+ * max_new, ctx_len[i] plus that <= max_total <= max_pages * page_size.  Kernels
+ * are chosen by them, and rglru_paged_append launches for max_new tokens of each
+ * of the S sequences, so they should lie near what they bound.  The lengths and
+ * the table live on the device, so they are checked there: a sequence whose
+ * lengths break the bounds is skipped, a page number outside the
  * pool is not touched (its tokens are not stored, or its keys not attended), and
  * RGLRU_ERR_INVALID_ARG is recorded in the workspace (rglru_get_device_status).
  * So is a cu_tokens that goes back somewhere (a negative count), without which

@@ -707,8 +707,12 @@ extern "C" RGLRU_API rglru_status rglru_linear_w4(int M, int N, int K, int group
     auto log2i = [](int v) { int s = 0; while ((1 << s) < v) ++s; return s; };
     const W4Args p = {M, N, K, log2i(group), A_scale ? log2i(a_group) : 0, debug_withheld, A, A_scale, static_cast<const uint8_t *>(W),
                       static_cast<const uint16_t *>(W_scale), bias, static_cast<__nv_bfloat16 *>(out)};
-    // Up to 16 rows the first kernel is as fast or faster at every size measured (16 rows of 12288 x 4096: 35 us both;
-    // 8 rows of 7680 x 2560 13 us against 20; one row of 2560 x 2560 10 against 14).
+    // Up to 16 rows the first kernel is the faster one at every size measured, by 2 to 4 us where x is e4m3 and there are two
+    // row tiles of it, by 4 to 15 otherwise.  First and second kernel, us behind a flush of L2, groups of 128, x in bf16 (e4m3):
+    //   rows    2560 x 2560             7680 x 2560             12288 x 4096
+    //      1     6 and 11 ( 7 and 12)   10 and 18 (10 and 19)   19 and 32 (20 and 33)
+    //      8     7 and 12 ( 7 and 12)   10 and 18 (11 and 19)   19 and 33 (21 and 34)
+    //     16     8 and 12 ( 9 and 13)   12 and 19 (16 and 20)   22 and 34 (32 and 34)
     if (M <= 16) return M <= 8 ? launch_few<1>(p, stream) : launch_few<2>(p, stream);
     switch ((M + 15) / 16) {
     case 2: return launch_tc<32>(p, stream);

@@ -49,8 +49,9 @@ struct Meta {                // of one tile in the ring, written by the producer
 
 template <int D>
 struct Cfg {
-    // three CTAs with few slots rather than two with more: a tile's chain is latency (256 sequences over 2048 keys, D 256:
-    // 62 us against 67; two CTAs with three slots take 67 as well)
+    // three CTAs with few slots rather than two with more: a tile's chain is latency (256 sequences over 2048 keys, D 256,
+    // behind a flush of L2: 70.0 us against 72.4; two CTAs with three slots 71.6; the same over 2000 keys of four heads of
+    // 128, 200 sequences: 86 against 100)
     static constexpr int kCtasPerSm = 3;
     static constexpr int kHalf = kKeyTile * 128;      // 64 keys x 128 channels (one swizzled box column)
     static constexpr int kSlotBytes = kKeyTile * D;   // k or v of a tile
@@ -1505,13 +1506,16 @@ rglru_status launch(const AttendArgs &p, cudaStream_t stream)
     static PerDeviceFlag flag, wide_flag;
     CUtensorMap tm_k, tm_v;
     if (!encode_pool(&tm_k, p.k, p.b) || !encode_pool(&tm_v, p.v, p.b)) return RGLRU_ERR_CUDA;
-    // A tile takes the 128-row kernel about 1.3 us an SM whatever its rows, the 16-row one 0.9: from three units of 16 rows on the
-    // first is ahead.  Short runs in the same batch go along with it (a second launch and its join cost 6 us).
+    // A tile takes the 128-row kernel about 1.3 us an SM whatever its rows, the 16-row one 0.9 for each unit of 16 rows.  256
+    // sequences of 32 rows over 2048 keys: 125 us and 112, of 48 rows 126 and 156; 64 sequences of 32 rows 43 and 44, of 48
+    // rows 42 and 57; 5 sequences of 48 rows 26 and 23, of 96 rows 27 and 26.  Short runs in the same batch go along with the
+    // long ones (a second launch and its join cost 6 us).
     if ((int64_t)p.b.max_new * (p.b.H / p.b.Hkv) <= 2 * kRowTile) {
         const rglru_status st = set_smem_limit_once(reinterpret_cast<const void *>(rglru_paged_attention_kernel<D>), C::kSmem, flag);
         if (st != RGLRU_OK) return st;
-        // A third CTA an SM pays when there is much to do (the figures at Cfg); with little, more pieces are more to join
-        // (one sequence over 131072 keys, 2048 tiles: 444 pieces 30.6 us, 296 28.8).
+        // A third CTA an SM pays when there is much to do (5280 tiles, 160 sequences: 50.5 us against 52.3; 8448: the figures
+        // at Cfg); with little, more pieces can be more to join (one sequence over 131072 keys, 2049 tiles: 444 pieces 30.5
+        // us, 296 29.1; 96 sequences, 3168 tiles: 39.4 and 38.7; but 64 sequences, 2112 tiles: 31.4 and 32.6).
         const int reach = p.window < p.b.max_total - p.b.max_new ? p.window + p.b.max_new : p.b.max_total;
         const int64_t tiles = (int64_t)p.b.S * p.b.Hkv * (reach / kKeyTile + 1);
         const int grid = kSms * (tiles < kManyTiles * kSms * C::kCtasPerSm ? 2 : C::kCtasPerSm);
@@ -1523,7 +1527,7 @@ rglru_status launch(const AttendArgs &p, cudaStream_t stream)
     if (st != RGLRU_OK) return st;
     // What keys below f16's range lose is at most 2^-(25 + top) a key: over 2^20 keys 2^-12 of the largest with a raise of
     // 2^8, so beyond them the reference follows every maximum (2^-10 over 2^30 keys).  Five chunks of up to 256 tokens over
-    // 2048 keys: 44.9 us against 48.8.
+    // 2048 keys: 45.1 us against 49.
     const int64_t reach = (int64_t)p.window + p.b.max_new < p.b.max_total ? (int64_t)p.window + p.b.max_new : p.b.max_total;
     AttendArgs a = p;
     a.raise = reach <= (1 << 20) ? 8.f : 0.f;
